@@ -56,8 +56,12 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 // copies: their base addresses must be 16-byte aligned.
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0u; }
 
+// Rows per (sequence, local KV group) of a compacted local cache.
+long long local_rows(const sd_ctx *ctx) { return (long long)ctx->cfg.num_sinks + ctx->cfg.window; }
+
 struct WsLayout {
   size_t scores_off, flags_off, scores_bytes, stream_off, stream_bytes, att_off, total;
+  size_t total_mass;                  // for the calls that accumulate weights
 };
 
 WsLayout layout(const sd_ctx *ctx, int batch) {
@@ -70,6 +74,7 @@ WsLayout layout(const sd_ctx *ctx, int batch) {
   w.stream_bytes = align256(sd::stream_workspace_bytes(ctx->sh, ctx->tb, batch, ctx->cfg.mode));
   w.att_off = w.stream_off + w.stream_bytes;
   w.total = align256(w.att_off + sd::attend_workspace_bytes(ctx->sh, ctx->tb, batch));
+  w.total_mass = align256(w.att_off + sd::attend_mass_workspace_bytes(ctx->sh, ctx->tb, batch, local_rows(ctx)));
   return w;
 }
 
@@ -80,29 +85,39 @@ long long max_topk(const sd_ctx *ctx) {
   return std::min(k, L);
 }
 
-// Rows per (sequence, local KV group) of a compacted local cache.
-long long local_rows(const sd_ctx *ctx) { return (long long)ctx->cfg.num_sinks + ctx->cfg.window; }
-
 // attend, alone (joined = false) or after the selection of the same sets
 // (joined = true), on the full paged caches (split = false) or on caches of the
-// retrieval groups plus compacted local caches (split = true)
+// retrieval groups plus compacted local caches (split = true); on 4-bit records
+// instead of k_cache / v_cache when form.kv4; adding the weights to form.mass
+// when that is not null
+struct AttendForm {
+  bool kv4 = false;
+  const void *records = nullptr;
+  float *mass = nullptr;
+};
+
 sd_status attend_impl(sd_ctx *ctx, const void *q_pre, const void *q, const void *index_cache, const void *k_cache,
                       const void *v_cache, const void *local_k, const void *local_v, const int32_t *page_table,
                       const int32_t *seq_lens, int batch, int32_t *sel_idx, int32_t *sel_count, int sel_stride,
-                      float *out, void *workspace, size_t ws_bytes, sd_stream stream, bool joined, bool split) {
+                      float *out, void *workspace, size_t ws_bytes, sd_stream stream, bool joined, bool split,
+                      const AttendForm &form = AttendForm()) {
   if (!ctx) return SD_ERR_INVALID_ARG;
   if (batch < 0 || batch > ctx->cfg.max_batch) return fail(ctx, SD_ERR_INVALID_ARG, "batch out of range");
   if (batch == 0) return SD_OK;
   const bool ret = ctx->sh.H_ret > 0;
   if (!q || !page_table || !seq_lens || !out) return fail(ctx, SD_ERR_INVALID_ARG, "null pointer");
   // with the split layout, caches of a kind of head that is absent may be NULL
-  const bool need_paged = !split || ret;
+  const bool need_paged = !form.kv4 && (!split || ret);
   const bool need_local = split && ctx->tb.n_loc > 0 && local_rows(ctx) > 0;
   if (need_paged && (!k_cache || !v_cache)) return fail(ctx, SD_ERR_INVALID_ARG, "null pointer");
   if (need_local && (!local_k || !local_v)) return fail(ctx, SD_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(q) || (need_paged && (!aligned16(k_cache) || !aligned16(v_cache))) ||
       (need_local && (!aligned16(local_k) || !aligned16(local_v))))
     return fail(ctx, SD_ERR_INVALID_ARG, "q and the K/V caches must be 16-byte aligned");
+  if (form.kv4 && !form.records) return fail(ctx, SD_ERR_INVALID_ARG, "null pointer");
+  if (form.kv4 && !aligned16(form.records))
+    return fail(ctx, SD_ERR_INVALID_ARG, "kv4_cache must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(form.mass) & 3u) return fail(ctx, SD_ERR_INVALID_ARG, "mass must be 4-byte aligned");
   // local cache rows are addressed with 32-bit row numbers inside the kernels
   if (need_local && (long long)batch * ctx->tb.n_loc * local_rows(ctx) >= 0xFFFFFFFFLL)
     return fail(ctx, SD_ERR_UNSUPPORTED, "local caches too large for 32-bit row numbers");
@@ -120,7 +135,8 @@ sd_status attend_impl(sd_ctx *ctx, const void *q_pre, const void *q, const void 
     }
   }
   const WsLayout w = layout(ctx, batch);
-  if (!workspace || ws_bytes < w.total) return fail(ctx, SD_ERR_WORKSPACE, "workspace too small");
+  if (!workspace || ws_bytes < (form.mass ? w.total_mass : w.total))
+    return fail(ctx, SD_ERR_WORKSPACE, "workspace too small");
   DeviceGuard dg(ctx->device);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   char *wsb = static_cast<char *>(workspace);
@@ -168,6 +184,8 @@ sd_status attend_impl(sd_ctx *ctx, const void *q_pre, const void *q, const void 
   at.split = split;
   at.local_k = static_cast<const uint16_t *>(local_k);
   at.local_v = static_cast<const uint16_t *>(local_v);
+  at.kv4 = static_cast<const uint8_t *>(form.records);
+  at.mass = form.mass;
   // with the union lists built by select, attend plans only the items the
   // exact selector redid (listed in the miss array)
   const uint32_t *only = unioned ? reinterpret_cast<const uint32_t *>(wsb + w.flags_off) : nullptr;
@@ -280,6 +298,7 @@ sd_status sparse_decode_init(const sd_config *cfg, const void *proj, sd_ctx **ou
     ctx->tb.n_loc = (int)ctx->loc_h.size();
     for (auto &g : ctx->ret_h) ctx->tb.max_ret = std::max(ctx->tb.max_ret, g.n);
     for (auto &g : ctx->loc_h) ctx->tb.max_loc = std::max(ctx->tb.max_loc, g.n);
+    ctx->tb.mixed = ctx->ret_h.size() + ctx->loc_h.size() > (size_t)Hkv;
     *out = holder.release();
     return SD_OK;
   } catch (...) {
@@ -550,6 +569,165 @@ sd_status sparse_decode_attend_noalloc(sd_ctx *ctx, const void *q, const void *k
     a.batch = batch;
     e = sd::launch_attend(a, ctx->sh, ctx->tb, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SD_OK : cuda_fail(ctx, e, "attend launch");
+  } catch (...) {
+    return SD_ERR_HOST_MEMORY;
+  }
+}
+
+sd_status sparse_decode_mass_workspace_size(const sd_ctx *ctx, int batch, size_t *bytes) {
+  try {
+    if (!ctx || !bytes) return SD_ERR_INVALID_ARG;
+    if (batch < 0 || batch > ctx->cfg.max_batch) return SD_ERR_INVALID_ARG;
+    *bytes = layout(ctx, batch).total_mass;
+    return SD_OK;
+  } catch (...) {
+    return SD_ERR_HOST_MEMORY;
+  }
+}
+
+sd_status sparse_decode_kv4_append(sd_ctx *ctx, const void *k_new, const void *v_new, const int32_t *slots,
+                                   int num_tokens, void *kv4_cache, sd_stream stream) {
+  try {
+    if (!ctx) return SD_ERR_INVALID_ARG;
+    if (num_tokens < 0) return fail(ctx, SD_ERR_INVALID_ARG, "num_tokens < 0");
+    if (num_tokens == 0) return SD_OK;
+    if (!k_new || !v_new || !slots || !kv4_cache) return fail(ctx, SD_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(kv4_cache))
+      return fail(ctx, SD_ERR_INVALID_ARG, "k_new, v_new and kv4_cache must be 16-byte aligned");
+    DeviceGuard dg(ctx->device);
+    const cudaError_t e = sd::launch_kv4_append(
+        static_cast<const uint16_t *>(k_new), static_cast<const uint16_t *>(v_new), slots, num_tokens,
+        static_cast<uint8_t *>(kv4_cache), ctx->sh, ctx->err_d, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SD_OK : cuda_fail(ctx, e, "kv4_append launch");
+  } catch (...) {
+    return SD_ERR_HOST_MEMORY;
+  }
+}
+
+sd_status sparse_decode_kv4_load(sd_ctx *ctx, const void *kv4_cache, const int32_t *slots, int num_tokens,
+                                 void *k_out, void *v_out, sd_stream stream) {
+  try {
+    if (!ctx) return SD_ERR_INVALID_ARG;
+    if (num_tokens < 0) return fail(ctx, SD_ERR_INVALID_ARG, "num_tokens < 0");
+    if (num_tokens == 0) return SD_OK;
+    if (!kv4_cache || !slots || !k_out || !v_out) return fail(ctx, SD_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(kv4_cache) || !aligned16(k_out) || !aligned16(v_out))
+      return fail(ctx, SD_ERR_INVALID_ARG, "kv4_cache, k_out and v_out must be 16-byte aligned");
+    DeviceGuard dg(ctx->device);
+    const cudaError_t e = sd::launch_kv4_load(static_cast<const uint8_t *>(kv4_cache), slots, num_tokens,
+                                              static_cast<uint16_t *>(k_out), static_cast<uint16_t *>(v_out), ctx->sh,
+                                              ctx->err_d, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SD_OK : cuda_fail(ctx, e, "kv4_load launch");
+  } catch (...) {
+    return SD_ERR_HOST_MEMORY;
+  }
+}
+
+sd_status sparse_decode_attend_kv4(sd_ctx *ctx, const void *q, const void *kv4_cache, const int32_t *page_table,
+                                   const int32_t *seq_lens, int batch, const int32_t *sel_idx,
+                                   const int32_t *sel_count, int sel_stride, float *out, float *mass,
+                                   void *workspace, size_t ws_bytes, sd_stream stream) {
+  try {
+    AttendForm form;
+    form.kv4 = true;
+    form.records = kv4_cache;
+    form.mass = mass;
+    return attend_impl(ctx, nullptr, q, nullptr, nullptr, nullptr, nullptr, nullptr, page_table, seq_lens, batch,
+                       const_cast<int32_t *>(sel_idx), const_cast<int32_t *>(sel_count), sel_stride, out, workspace,
+                       ws_bytes, stream, false, false, form);
+  } catch (...) {
+    return SD_ERR_HOST_MEMORY;
+  }
+}
+
+sd_status sparse_decode_select_attend_kv4(sd_ctx *ctx, const void *q_pre, const void *q, const void *index_cache,
+                                          const void *kv4_cache, const int32_t *page_table, const int32_t *seq_lens,
+                                          int batch, int32_t *sel_idx, int32_t *sel_count, int sel_stride, float *out,
+                                          float *mass, void *workspace, size_t ws_bytes, sd_stream stream) {
+  try {
+    AttendForm form;
+    form.kv4 = true;
+    form.records = kv4_cache;
+    form.mass = mass;
+    return attend_impl(ctx, q_pre, q, index_cache, nullptr, nullptr, nullptr, nullptr, page_table, seq_lens, batch,
+                       sel_idx, sel_count, sel_stride, out, workspace, ws_bytes, stream, true, false, form);
+  } catch (...) {
+    return SD_ERR_HOST_MEMORY;
+  }
+}
+
+sd_status sparse_decode_attend_mass(sd_ctx *ctx, const void *q, const void *k_cache, const void *v_cache,
+                                    const int32_t *page_table, const int32_t *seq_lens, int batch,
+                                    const int32_t *sel_idx, const int32_t *sel_count, int sel_stride, float *out,
+                                    float *mass, void *workspace, size_t ws_bytes, sd_stream stream) {
+  try {
+    if (ctx && batch != 0 && !mass) return fail(ctx, SD_ERR_INVALID_ARG, "null pointer");
+    AttendForm form;
+    form.mass = mass;
+    return attend_impl(ctx, nullptr, q, nullptr, k_cache, v_cache, nullptr, nullptr, page_table, seq_lens, batch,
+                       const_cast<int32_t *>(sel_idx), const_cast<int32_t *>(sel_count), sel_stride, out, workspace,
+                       ws_bytes, stream, false, false, form);
+  } catch (...) {
+    return SD_ERR_HOST_MEMORY;
+  }
+}
+
+sd_status sparse_decode_select_attend_mass(sd_ctx *ctx, const void *q_pre, const void *q, const void *index_cache,
+                                           const void *k_cache, const void *v_cache, const int32_t *page_table,
+                                           const int32_t *seq_lens, int batch, int32_t *sel_idx, int32_t *sel_count,
+                                           int sel_stride, float *out, float *mass, void *workspace, size_t ws_bytes,
+                                           sd_stream stream) {
+  try {
+    if (ctx && batch != 0 && !mass) return fail(ctx, SD_ERR_INVALID_ARG, "null pointer");
+    AttendForm form;
+    form.mass = mass;
+    return attend_impl(ctx, q_pre, q, index_cache, k_cache, v_cache, nullptr, nullptr, page_table, seq_lens, batch,
+                       sel_idx, sel_count, sel_stride, out, workspace, ws_bytes, stream, true, false, form);
+  } catch (...) {
+    return SD_ERR_HOST_MEMORY;
+  }
+}
+
+sd_status sparse_decode_evict(sd_ctx *ctx, float *mass, const int32_t *page_table, const int32_t *seq_lens, int batch,
+                              const int32_t *new_page_table, int budget, int keep_first, int keep_last, int32_t *kept,
+                              int32_t *new_lens, void *k_cache, void *v_cache, void *index_cache, void *kv4_cache,
+                              sd_stream stream) {
+  try {
+    if (!ctx) return SD_ERR_INVALID_ARG;
+    if (batch < 0 || batch > ctx->cfg.max_batch) return fail(ctx, SD_ERR_INVALID_ARG, "batch out of range");
+    if (batch == 0) return SD_OK;
+    if (!mass || !page_table || !seq_lens || !new_page_table || !kept || !new_lens)
+      return fail(ctx, SD_ERR_INVALID_ARG, "null pointer");
+    if (budget < 1 || budget > ctx->sh.max_len) return fail(ctx, SD_ERR_INVALID_ARG, "budget outside [1, L]");
+    if (keep_first < 0 || keep_last < 0 || (long long)keep_first + keep_last > budget)
+      return fail(ctx, SD_ERR_INVALID_ARG, "keep_first + keep_last outside [0, budget]");
+    if (new_page_table == page_table || new_lens == seq_lens)
+      return fail(ctx, SD_ERR_INVALID_ARG, "the new pages and lengths must not be the old ones");
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(index_cache) || !aligned16(kv4_cache))
+      return fail(ctx, SD_ERR_INVALID_ARG, "the caches must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(mass) & 3u) return fail(ctx, SD_ERR_INVALID_ARG, "mass must be 4-byte aligned");
+    DeviceGuard dg(ctx->device);
+    const int d = ctx->sh.d;
+    sd::EvictArgs a{};
+    a.mass = mass;
+    a.page_table = page_table;
+    a.seq_lens = seq_lens;
+    a.new_page_table = new_page_table;
+    a.kept = kept;
+    a.new_lens = new_lens;
+    a.batch = batch;
+    a.budget = budget;
+    a.keep_first = keep_first;
+    a.keep_last = keep_last;
+    void *const caches[4] = {k_cache, v_cache, index_cache, kv4_cache};
+    const int bytes[4] = {2 * d, 2 * d, 2 * sd::kIndexDim, sd::kv4_record_bytes(d)};
+    for (int k = 0; k < 4; ++k) {
+      a.cache[k] = static_cast<uint8_t *>(caches[k]);
+      a.row_bytes[k] = bytes[k];
+    }
+    a.err = ctx->err_d;
+    const cudaError_t e = sd::launch_evict(a, ctx->sh, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SD_OK : cuda_fail(ctx, e, "evict launch");
   } catch (...) {
     return SD_ERR_HOST_MEMORY;
   }

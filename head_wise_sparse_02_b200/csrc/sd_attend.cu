@@ -43,16 +43,11 @@
 //         partial (m, l, acc[d]) and the last to finish (atomic ticket, no
 //         waiting) merges the partials with a log-sum-exp combine.
 #include <algorithm>
-#include <map>
-#include <mutex>
 
-#include "sd_internal.cuh"
+#include "sd_attend.cuh"
 
 namespace sd {
 namespace {
-
-constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr float kLog2e = 1.4426950408889634f;
 
 // plan
 constexpr int kPlanThreads = 256;
@@ -60,141 +55,8 @@ constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kSpanMax = 32768;         // positions per plan CTA (max)
 constexpr int kPlanCtas = 296;          // plan CTAs aimed for when the items are few (two per SM)
 
-// main
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
-constexpr int kTileRows = 16;
-constexpr int kTileRing = 3;            // tiles in flight per warp
-constexpr int kMaxGrid = 4096;          // persistent CTAs (partial slots are sized for this)
-constexpr int kMergeChunk = 64;         // partial slots weighed per step of the final merge
+constexpr int kTileRing = 3;            // tiles in flight per warp (bf16 main kernel)
 constexpr int kDensePlanBits = 256;     // union bits per warp step above which lanes write their own rows
-
-// 16-byte copy global -> shared, bypassing L1, with an L2 eviction-priority
-// hint (see evict_first_policy)
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int src_bytes, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;\n" ::"r"(dst), "l"(src),
-               "r"(src_bytes), "l"(policy)
-               : "memory");
-}
-
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-// d += a * b, bf16 inputs, float32 accumulate
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// the same with rows 8-15 of A zero: only d0, d1 (rows 0-7) are kept, so the
-// accumulators of the empty rows need no registers; zu / zf hold 0 (kept in
-// one register each by the caller)
-__device__ __forceinline__ void mma_bf16_top(float (&d)[2], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1,
-                                             uint32_t zu, float zf) {
-  [[maybe_unused]] float j0, j1;                    // outputs of the empty rows, discarded
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, "
-      "{%0,%1,%9,%9};\n"
-      : "+f"(d[0]), "+f"(d[1]), "=f"(j0), "=f"(j1)
-      : "r"(a0), "r"(zu), "r"(a2), "r"(b0), "r"(b1), "f"(zf));
-}
-// 2^x by the MUFU unit (PTX ex2.approx.ftz.f32: relative error below 2^-22,
-// subnormal results flushed to 0, exp2(-inf) = 0), far inside the float32
-// accumulation's own error here
-__device__ __forceinline__ float fast_exp2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
-  return r;
-}
-// two floats -> bf16x2 (x in the low half), round to nearest even
-__device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(y), "f"(x));
-  return r;
-}
-// p = hi + lo with hi = bf16(p), lo = bf16(p - hi): |p - hi - lo| <= 2^-17 |p|
-__device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint32_t &lo) {
-  hi = pack_bf16(x, y);
-  lo = pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi));
-}
-
-// First index i in [0, n) with arr[i] >= x (n if none), arr ascending; the
-// whole warp cooperates.  While the bracket is wider than 31, each lane
-// probes 4 of 128 evenly spaced points, the last of which lies at or past hi
-// (one dependent round narrows the bracket ~127-fold); then lane j probes
-// lo + j, and lane 31 lands at or past hi.  Either way some lane is true.
-template <typename T>
-__device__ int warp_lower_bound(const T *arr, int n, T x, int lane) {
-  int lo = 0, hi = n;                      // answer in [lo, hi]
-  while (hi - lo > 31) {
-    const int step = (hi - lo + 126) / 127;  // 127 * step >= hi - lo: probe 127 is past hi
-    bool ge[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int p = lo + (lane * 4 + j) * step;
-      ge[j] = (p < hi) ? (__ldcg(arr + p) >= x) : true;
-    }
-    const int jf = ge[0] ? 0 : (ge[1] ? 1 : (ge[2] ? 2 : (ge[3] ? 3 : 4)));
-    const unsigned bal = __ballot_sync(kFull, jf < 4);
-    // probe k = 4 l + j is at lo + k step; probe 127 (lane 31) is always true
-    const int l = __ffs(bal) - 1;
-    const int first = l * 4 + __shfl_sync(kFull, jf, l);
-    const int nhi = std::min(hi, lo + first * step);
-    const int nlo = first == 0 ? lo : lo + (first - 1) * step + 1;
-    lo = nlo;
-    hi = nhi;
-  }
-  const int p = lo + lane;                 // hi - lo <= 31: lane 31 is past hi
-  const bool ge = (p < hi) ? (__ldcg(arr + p) >= x) : true;
-  return lo + (__ffs(__ballot_sync(kFull, ge)) - 1);
-}
-
-struct AttParams {
-  int span;                 // plan: positions per span (power of two, multiple of 32)
-  int ns;                   // plan: spans per sequence
-  int n_ret_items;          // B * n_ret retrieval items, numbered first
-  int ni;                   // all items: then B * n_loc local items
-};
-
-// Carving of the attend workspace.
-struct AttWs {
-  float *partials;          // [(kMaxGrid + ni) slots][GR][D + 2]
-  uint32_t *plan_row;       // [B][n_ret][ns][span]: cache row of each union entry
-  uint16_t *plan_mask;      // [B][n_ret][ns][span]: heads (bit i = i-th head of the group)
-  int *plan_cnt;            // [B][n_ret][ns]
-  long long *tstart;        // [ni + 1]: first tile of each item; tstart[ni] = all tiles
-  int *item_rows;           // [ni]: rows of each item (layout)
-  unsigned *tickets;        // [ni]: partials merged per item (cleared by the layout)
-};
-
-__device__ __forceinline__ const Group &item_group(const Tables &tb, const AttParams &ap, int i, int &b,
-                                                   bool &is_ret) {
-  is_ret = i < ap.n_ret_items;
-  if (is_ret) {
-    b = i / tb.n_ret;
-    return tb.ret[i % tb.n_ret];
-  }
-  const int j = i - ap.n_ret_items;
-  b = j / tb.n_loc;
-  return tb.loc[j % tb.n_loc];
-}
-
-__device__ __forceinline__ long long clamp_len(const AttendArgs &a, const Shape &sh, int b) {
-  const long long N = a.seq_lens[b];
-  return N < 0 ? 0 : std::min<long long>(N, sh.max_len);
-}
 
 // Tile counts and first tiles of all items, by one CTA (block size a multiple
 // of 32, at most 1024).  A retrieval item's rows are the sum of its spans'
@@ -455,20 +317,16 @@ attend_plan_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
 }
 
 // ============================================================== main kernel
-struct MainShared {
-  Group grp;
-  int item;                 // current item
-  int last;
-};
-
 // dynamic shared memory: [ring: kWarps x kTileRing x (16 K rows + 16 V rows),
 //                         rows padded to 2d + 16 bytes: ldmatrix phases hit
 //                         distinct banks and every offset is a constant]
 //                        [head masks of the tiles in the rings: kWarps x kTileRing x 16 x uint16]
 //                        [span prefix of the current item: ns + 1 ints]
 // between items the ring holds the warps' (m, l, acc) for the CTA merge
-template <int D, int GR>
-__global__ void __launch_bounds__(kThreads)
+// MASS: every logit, with its tile's cache rows, is left in the workspace for
+// the weights pass (sd_mass.cu)
+template <int D, int GR, bool MASS>
+__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 1)
 attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const AttParams ap, const AttWs ws) {
   constexpr int KS = D / 16;                         // k-steps of Q K^T
   constexpr int NT = D / 8;                          // n-tiles (8 dims) of P V
@@ -636,6 +494,14 @@ attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
     // data) and are masked out; the masks go to the warp's slot of tile q
     auto prep = [&](int q, uint32_t row, uint32_t mask) -> uint32_t {
       if (q < mt) {
+        if constexpr (MASS) {
+          // columns in the order the score fragments hold them: column
+          // 4 tq + 2 j + e is row 8 j + 2 tq + e
+          const long long tile = t + warp + (long long)q * kWarps;
+          if (lane < kTileRows)
+            ws.tile_row[tile * kTileRows + ((lane >> 1) & 3) * 4 + (lane >> 3) * 2 + (lane & 1)] = mask ? row : kNoRow;
+          if (lane == 0) ws.tile_item[tile] = item;
+        }
         const long long gx0 = r0 + (long long)(warp + q * kWarps) * kTileRows;
         const uint32_t first = __shfl_sync(kFull, row, 0);
         if (gx0 + (lane & 15) >= r1) row = first;
@@ -709,6 +575,12 @@ attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
             p[j][e] = (mm & head_bit0) ? s[j][e] * sc : -INFINITY;
             p[j][2 + e] = (HI && (mm & head_bit1)) ? s[j][2 + e] * sc : -INFINITY;
           }
+        if constexpr (MASS) {
+          float *lg = ws.logits + ((t + warp + (long long)q * kWarps) * GR) * kTileRows + 4 * tq;
+          if (gq < nh) *reinterpret_cast<float4 *>(lg + gq * kTileRows) = make_float4(p[0][0], p[0][1], p[1][0], p[1][1]);
+          if (HI && gq + 8 < nh)
+            *reinterpret_cast<float4 *>(lg + (gq + 8) * kTileRows) = make_float4(p[0][2], p[0][3], p[1][2], p[1][3]);
+        }
         // online softmax per head (head gq: p[.][0..1]; head gq + 8: p[.][2..3])
         float x0m = fmaxf(fmaxf(p[0][0], p[0][1]), fmaxf(p[1][0], p[1][1]));
         x0m = fmaxf(x0m, __shfl_xor_sync(kFull, x0m, 1));
@@ -810,121 +682,7 @@ attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
         cacc[(warp * GR + gq + 8) * D + cc + 1] = o[nn][3];
       }
     }
-    __syncthreads();
-    const bool alone = first == last;                  // the whole item is in this CTA
-    float *part = ws.partials + ((c + item) * GR) * (long long)(D + 2);
-    for (int x = tid; x < nh * (D + 2); x += kThreads) {
-      const int i = x / (D + 2), cc = x % (D + 2);
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, cm[w * 16 + i]);
-      if (alone) {
-        if (cc < 2) continue;
-        float num = 0.0f, den = 0.0f;
-        if (M > -INFINITY) {
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float f = exp2f(cm[w * 16 + i] - M);
-            den = fmaf(f, cl[w * 16 + i], den);
-            num = fmaf(f, cacc[(w * GR + i) * D + (cc - 2)], num);
-          }
-        }
-        a.out[((long long)b * sh.Hq + S.grp.q_head[i]) * D + (cc - 2)] = den > 0.0f ? num / den : 0.0f;
-        continue;
-      }
-      float v;
-      if (cc == 0) {
-        v = M;
-      } else {
-        v = 0.0f;
-        if (M > -INFINITY) {
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float f = exp2f(cm[w * 16 + i] - M);
-            v += f * (cc == 1 ? cl[w * 16 + i] : cacc[(w * GR + i) * D + (cc - 2)]);
-          }
-        }
-      }
-      part[i * (D + 2) + cc] = v;
-    }
-    if (!alone) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) S.last = (atomicAdd(ws.tickets + item, 1u) == (unsigned)(last - first));
-      __syncthreads();
-      if (S.last) {
-        __threadfence();
-        // the last segment of the item: merge partial slots first + item .. last
-        // + item.  Per head i the reference M_i = max_s m_s; then, kMergeChunk
-        // slots at a time, the weights f_is = 2^(m_s - M_i) (0 for an empty
-        // slot) go to shared memory and every output sums f_is o_s[cc] with
-        // independent loads (an item can span a few hundred CTAs)
-        const int np = (int)(last - first + 1);
-        constexpr long long PS = (long long)GR * (D + 2);            // stride of the partial slots
-        constexpr int OPT = (GR * D + kThreads - 1) / kThreads;     // outputs per thread, at most
-        const float *pbase = ws.partials + (first + item) * PS;
-        float *fw = reinterpret_cast<float *>(dyn);                  // [GR][kMergeChunk]
-        float *sM = fw + GR * kMergeChunk;                           // [GR]
-        float *sden = sM + GR;                                       // [GR]
-        for (int i = warp; i < nh; i += kWarps) {
-          float M = -INFINITY;
-          for (int s = lane; s < np; s += 32) M = fmaxf(M, __ldcg(pbase + s * PS + i * (D + 2)));
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
-          if (lane == 0) {
-            sM[i] = M;
-            sden[i] = 0.0f;
-          }
-        }
-        float num[OPT];
-#pragma unroll
-        for (int u = 0; u < OPT; ++u) num[u] = 0.0f;
-        for (int s0 = 0; s0 < np; s0 += kMergeChunk) {
-          const int nc = np - s0 < kMergeChunk ? np - s0 : kMergeChunk;
-          __syncthreads();                             // M ready; the previous chunk's weights consumed
-          for (int x = tid; x < nh * kMergeChunk; x += kThreads) {
-            const int i = x / kMergeChunk, sl = x % kMergeChunk;
-            float f = 0.0f;
-            if (sl < nc) {
-              const float ms = __ldcg(pbase + (s0 + sl) * PS + i * (D + 2));
-              f = (ms == -INFINITY || sM[i] == -INFINITY) ? 0.0f : exp2f(ms - sM[i]);
-            }
-            fw[i * kMergeChunk + sl] = f;
-          }
-          __syncthreads();
-          for (int i = warp; i < nh; i += kWarps) {
-            float dsum = 0.0f;
-            for (int sl = lane; sl < nc; sl += 32)
-              dsum = fmaf(fw[i * kMergeChunk + sl], __ldcg(pbase + (s0 + sl) * PS + i * (D + 2) + 1), dsum);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) dsum += __shfl_xor_sync(kFull, dsum, off);
-            if (lane == 0) sden[i] += dsum;
-          }
-#pragma unroll
-          for (int u = 0; u < OPT; ++u) {
-            const int x = tid + u * kThreads;
-            if (x < nh * D) {
-              const int i = x / D, cc = x % D;
-              const float *pp = pbase + s0 * PS + i * (D + 2) + 2 + cc;
-              const float *fi = fw + i * kMergeChunk;
-              float acc = num[u];
-#pragma unroll 8
-              for (int sl = 0; sl < nc; ++sl) acc = fmaf(fi[sl], __ldcg(pp + sl * PS), acc);
-              num[u] = acc;
-            }
-          }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < OPT; ++u) {
-          const int x = tid + u * kThreads;
-          if (x < nh * D) {
-            const int i = x / D, cc = x % D;
-            a.out[((long long)b * sh.Hq + S.grp.q_head[i]) * D + cc] = sden[i] > 0.0f ? num[u] / sden[i] : 0.0f;
-          }
-        }
-      }
-    }
+    merge_segment<D, GR, MASS>(a, sh, ws, S, dyn, GR, c, item, first, last, b, nh);
     t = seg_end;
     if (tid == 0) S.item = item + 1;
   }
@@ -957,9 +715,11 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct AttLayout {
   size_t partials, plan_row, plan_mask, plan_cnt, tstart, counters, total;
+  size_t logits, tile_row, tile_item, lse, total_mass;                // accumulated weights: behind the rest
 };
 
-AttLayout att_layout(const Shape &sh, const Tables &tb, int batch) {
+// local_rows: rows a local head can attend to (num_sinks + window)
+AttLayout att_layout(const Shape &sh, const Tables &tb, int batch, long long local_rows) {
   const AttParams p = att_params(sh, tb, batch);
   AttLayout L{};
   const size_t entries = (size_t)batch * tb.n_ret * p.ns * p.span;
@@ -971,44 +731,29 @@ AttLayout att_layout(const Shape &sh, const Tables &tb, int batch) {
   L.tstart = o;    o = align256(o + (size_t)(p.ni + 1) * 8);
   L.counters = o;  o = align256(o + (size_t)p.ni * 2 * 4);           // item_rows, tickets
   L.total = o;
+  const size_t loc_tiles = (size_t)((std::min(sh.max_len, local_rows) + kTileRows - 1) / kTileRows);
+  const size_t tiles = (size_t)batch * ((size_t)tb.n_ret * sh.max_pages + (size_t)tb.n_loc * loc_tiles);
+  L.logits = o;    o = align256(o + tiles * group_rows_att(tb) * kTileRows * sizeof(float));
+  L.tile_row = o;  o = align256(o + tiles * kTileRows * 4);
+  L.tile_item = o; o = align256(o + tiles * 4);
+  L.lse = o;       o = align256(o + (size_t)p.ni * kMaxGroup * sizeof(float2));
+  L.total_mass = o;
   return L;
 }
 
-template <typename K>
-cudaError_t set_smem(K kern, size_t bytes) {
-  static std::mutex mu;
-  static std::map<std::pair<const void *, int>, size_t> done;
-  int dev = 0;
-  cudaGetDevice(&dev);
-  std::lock_guard<std::mutex> lk(mu);
-  const auto key = std::make_pair((const void *)kern, dev);
-  auto it = done.find(key);
-  if (it != done.end() && it->second >= bytes) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) done[key] = bytes;
-  return e;
-}
-
-// resident CTAs of a kernel on this device (cached)
-template <typename K>
-int resident_ctas(K kern, int threads, size_t smem) {
-  static std::mutex mu;
-  static std::map<std::pair<const void *, int>, int> cache;
-  int dev = 0;
-  cudaGetDevice(&dev);
-  std::lock_guard<std::mutex> lk(mu);
-  const auto key = std::make_pair((const void *)kern, dev);
-  auto it = cache.find(key);
-  if (it != cache.end()) return it->second;
-  int occ = 0, sms = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, threads, smem) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return 0;                                        // not cached: retried next call
-  }
-  const int n = std::max(1, std::min(kMaxGrid, occ * sms));
-  cache.emplace(key, n);
-  return n;
+template <int D, int GR, bool MASS>
+cudaError_t launch_main(const AttendArgs &a, const Shape &sh, const Tables &tb, const AttParams &p, const AttWs &ws,
+                        cudaStream_t st) {
+  const size_t ring = (size_t)kWarps * kTileRing * (2 * kTileRows * (2 * D + 16));
+  const size_t lists = (size_t)kWarps * kTileRing * kTileRows * 2 + (size_t)(p.ns + 1) * 4;
+  const size_t merge = std::max((size_t)kWarps * 32 * 4 + (size_t)kWarps * GR * D * 4,
+                                (size_t)GR * (kMergeChunk + 2) * 4);
+  const size_t bytes = std::max(ring + lists, merge);
+  const cudaError_t e = set_smem(attend_main_kernel<D, GR, MASS>, bytes);
+  if (e != cudaSuccess) return e;
+  const int grid = resident_ctas(attend_main_kernel<D, GR, MASS>, kThreads, bytes);
+  if (grid <= 0) return cudaErrorInvalidConfiguration;
+  return launch_pdl(attend_main_kernel<D, GR, MASS>, dim3(grid), dim3(kThreads), bytes, st, 0, a, sh, tb, p, ws);
 }
 
 template <int D, int GR>
@@ -1026,16 +771,12 @@ cudaError_t launch_t(const AttendArgs &a, const Shape &sh, const Tables &tb, con
   }
   e = launch_pdl(attend_prefix_kernel<D>, dim3(1), dim3(1024), 0, st, 0, a, sh, tb, p, ws);
   if (e != cudaSuccess) return e;
-  const size_t ring = (size_t)kWarps * kTileRing * (2 * kTileRows * (2 * D + 16));
-  const size_t lists = (size_t)kWarps * kTileRing * kTileRows * 2 + (size_t)(p.ns + 1) * 4;
-  const size_t merge = std::max((size_t)kWarps * 32 * 4 + (size_t)kWarps * GR * D * 4,
-                                (size_t)GR * (kMergeChunk + 2) * 4);
-  const size_t bytes = std::max(ring + lists, merge);
-  e = set_smem(attend_main_kernel<D, GR>, bytes);
-  if (e != cudaSuccess) return e;
-  const int grid = resident_ctas(attend_main_kernel<D, GR>, kThreads, bytes);
-  if (grid <= 0) return cudaErrorInvalidConfiguration;
-  return launch_pdl(attend_main_kernel<D, GR>, dim3(grid), dim3(kThreads), bytes, st, 0, a, sh, tb, p, ws);
+  if (a.kv4)
+    e = launch_attend_kv4_main(a, sh, tb, p, ws, GR, st);
+  else
+    e = a.mass ? launch_main<D, GR, true>(a, sh, tb, p, ws, st) : launch_main<D, GR, false>(a, sh, tb, p, ws, st);
+  if (e != cudaSuccess || !a.mass) return e;
+  return launch_mass(a, tb, p, ws, GR, st);
 }
 
 template <int D>
@@ -1053,11 +794,15 @@ cudaError_t dispatch_gr(const AttendArgs &a, const Shape &sh, const Tables &tb, 
 }  // namespace
 
 size_t attend_workspace_bytes(const Shape &sh, const Tables &tb, int batch) {
-  return att_layout(sh, tb, batch).total;
+  return att_layout(sh, tb, batch, 0).total;
+}
+
+size_t attend_mass_workspace_bytes(const Shape &sh, const Tables &tb, int batch, long long local_rows) {
+  return att_layout(sh, tb, batch, local_rows).total_mass;
 }
 
 UnionOut attend_union_view(const Shape &sh, const Tables &tb, int batch, void *attend_ws, bool ret_only) {
-  const AttLayout L = att_layout(sh, tb, batch);
+  const AttLayout L = att_layout(sh, tb, batch, 0);
   const AttParams p = att_params(sh, tb, batch);
   char *base = static_cast<char *>(attend_ws);
   return UnionOut{reinterpret_cast<uint32_t *>(base + L.plan_row), reinterpret_cast<uint16_t *>(base + L.plan_mask),
@@ -1067,7 +812,7 @@ UnionOut attend_union_view(const Shape &sh, const Tables &tb, int batch, void *a
 cudaError_t launch_attend(const AttendArgs &a, const Shape &sh, const Tables &tb, cudaStream_t st,
                           const uint32_t *plan_only) {
   if (a.batch == 0) return cudaSuccess;
-  const AttLayout L = att_layout(sh, tb, a.batch);
+  const AttLayout L = att_layout(sh, tb, a.batch, (long long)a.num_sinks + a.window);
   const AttParams p = att_params(sh, tb, a.batch);
   char *base = static_cast<char *>(a.ws);
   AttWs ws{};
@@ -1078,6 +823,12 @@ cudaError_t launch_attend(const AttendArgs &a, const Shape &sh, const Tables &tb
   ws.tstart = reinterpret_cast<long long *>(base + L.tstart);
   ws.item_rows = reinterpret_cast<int *>(base + L.counters);
   ws.tickets = reinterpret_cast<unsigned *>(ws.item_rows + p.ni);
+  if (a.mass) {
+    ws.logits = reinterpret_cast<float *>(base + L.logits);
+    ws.tile_row = reinterpret_cast<uint32_t *>(base + L.tile_row);
+    ws.tile_item = reinterpret_cast<int *>(base + L.tile_item);
+    ws.lse = reinterpret_cast<float2 *>(base + L.lse);
+  }
   return sh.d == 128 ? dispatch_gr<128>(a, sh, tb, p, ws, st, plan_only)
                      : dispatch_gr<64>(a, sh, tb, p, ws, st, plan_only);
 }

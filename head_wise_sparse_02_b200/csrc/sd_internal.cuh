@@ -27,6 +27,7 @@ struct Tables {
   int n_ret, n_loc;
   int max_ret;                    // largest n over ret groups
   int max_loc;                    // largest n over loc groups
+  bool mixed;                     // a KV head has heads of both roles
 };
 
 struct Shape {
@@ -294,7 +295,46 @@ struct AttendArgs {
   bool split;
   const uint16_t *local_k;
   const uint16_t *local_v;
+  // 4-bit records instead of k_cache / v_cache (null = bf16 caches)
+  const uint8_t *kv4;
+  // accumulated weights [num_pages][Hkv][kPage] (null = not kept)
+  float *mass;
 };
+
+// ------------------------------------------------------------- 4-bit records
+// One record holds the key and the value of one token of one KV head, d
+// channels each in groups of 32 (NG = d / 32): 5 d / 4 bytes, so five 32-byte
+// sectors at d = 128.  A channel stands for lo + s code (code 0..15, s and lo
+// bf16, per group):
+//   d / 2 bytes  key codes: 32-bit word t NG + g, nibble e = channel 32 g + 8 t + e
+//   d / 2 bytes  value codes: 16-bit word c NG + g, nibble e = channel 32 g + 4 c + e
+//   d / 4 bytes  bf16: key s [NG], key lo [NG], value s [NG], value lo [NG]
+// Lane t of a quad finds its key words of all groups side by side (its part of
+// the contraction over the channels), lane c of eight its value channels of
+// all groups (its rows of the output).
+constexpr int kKv4Group = 32;
+__host__ __device__ constexpr int kv4_record_bytes(int d) { return d + d / 4; }
+
+cudaError_t launch_kv4_append(const uint16_t *k_new, const uint16_t *v_new, const int32_t *slots, int T,
+                              uint8_t *kv4, const Shape &sh, unsigned *err, cudaStream_t st);
+cudaError_t launch_kv4_load(const uint8_t *kv4, const int32_t *slots, int T, uint16_t *k_out, uint16_t *v_out,
+                            const Shape &sh, unsigned *err, cudaStream_t st);
+
+struct EvictArgs {
+  float *mass;                    // [num_pages][Hkv][kPage]
+  const int32_t *page_table;
+  const int32_t *seq_lens;
+  const int32_t *new_page_table;
+  int32_t *kept;                  // [B][Hkv][budget]
+  int32_t *new_lens;              // [B]
+  int batch;
+  int budget, keep_first, keep_last;
+  // caches whose rows move (null = absent): base and bytes of one row
+  uint8_t *cache[4];
+  int row_bytes[4];
+  unsigned *err;
+};
+cudaError_t launch_evict(const EvictArgs &a, const Shape &sh, cudaStream_t st);
 
 // Slot of position `pos` in a compacted local-head cache: sinks first, then a
 // ring of `window` slots; -1 when the position is kept nowhere (no window).
@@ -319,6 +359,8 @@ cudaError_t launch_local_append(const uint16_t *k_new, const uint16_t *v_new, co
                                 unsigned *err, cudaStream_t st);
 
 size_t attend_workspace_bytes(const Shape &sh, const Tables &tb, int batch);
+// with accumulated weights (AttendArgs::mass); local_rows = num_sinks + window
+size_t attend_mass_workspace_bytes(const Shape &sh, const Tables &tb, int batch, long long local_rows);
 // plan_only: null = plan every retrieval item; else the select's miss array
 // ([items] flags, count, list): only the listed items are planned, the
 // others' union lists are already in the workspace.

@@ -23,7 +23,7 @@ LIB_PATH = os.environ.get("SPARSE_DECODE_LIB") or os.path.join(
 SD_OK, SD_ERR_INVALID_ARG, SD_ERR_UNSUPPORTED, SD_ERR_WORKSPACE, SD_ERR_CUDA, SD_ERR_TIMEOUT, \
     SD_ERR_DEVICE_DATA, SD_ERR_HOST_MEMORY = range(8)
 SD_TOP_P, SD_TOP_K = 0, 1
-SD_EBIT_PAGE, SD_EBIT_SEQLEN, SD_EBIT_SEL, SD_EBIT_SLOT, SD_EBIT_TIMEOUT = 1, 2, 4, 8, 16
+SD_EBIT_PAGE, SD_EBIT_SEQLEN, SD_EBIT_SEL, SD_EBIT_SLOT, SD_EBIT_TIMEOUT, SD_EBIT_VALUE = 1, 2, 4, 8, 16, 32
 
 
 class SparseDecodeError(RuntimeError):
@@ -62,6 +62,15 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
                                                       c_size_t, P]),
         "sparse_decode_local_append": (c_int, [P, P, P, P, P, c_int, P, P, P]),
         "sparse_decode_prefill": (c_int, [P, P, P, P, P, P, P, c_int, c_int, P, P]),
+        "sparse_decode_mass_workspace_size": (c_int, [P, c_int, POINTER(c_size_t)]),
+        "sparse_decode_kv4_append": (c_int, [P, P, P, P, c_int, P, P]),
+        "sparse_decode_kv4_load": (c_int, [P, P, P, c_int, P, P, P]),
+        "sparse_decode_attend_kv4": (c_int, [P, P, P, P, P, c_int, P, P, c_int, P, P, P, c_size_t, P]),
+        "sparse_decode_select_attend_kv4": (c_int, [P, P, P, P, P, P, P, c_int, P, P, c_int, P, P, P, c_size_t, P]),
+        "sparse_decode_attend_mass": (c_int, [P, P, P, P, P, P, c_int, P, P, c_int, P, P, P, c_size_t, P]),
+        "sparse_decode_select_attend_mass": (c_int, [P, P, P, P, P, P, P, P, c_int, P, P, c_int, P, P, P, c_size_t,
+                                                     P]),
+        "sparse_decode_evict": (c_int, [P, P, P, P, c_int, P, c_int, c_int, c_int, P, P, P, P, P, P, P]),
         "sparse_decode_num_retrieval_groups": (c_int, [P]),
         "sparse_decode_num_local_groups": (c_int, [P]),
         "sparse_decode_head_er_workspace_size": (c_int, [c_int, c_int, c_int, c_int, POINTER(c_size_t)]),
@@ -128,9 +137,9 @@ def _check_sets(ctx: int, sel_idx, sel_count, batch: int) -> None:
         raise ValueError(f"sel_count must be [B >= {batch}, H_ret = {h_ret}], got {tuple(sel_count.shape)}")
 
 
-def _stream(stream) -> int:
+def _stream(stream, device=None) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch.cuda.current_stream(device).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -350,6 +359,137 @@ def sparse_decode_attend_noalloc(ctx: int, q, k_cache, v_cache, page_table, seq_
         _ptr(out, torch.float32, "out"), _stream(stream)), ctx)
 
 
+def sparse_decode_mass_workspace_size(ctx: int, batch: int) -> int:
+    """Workspace bytes of the calls with accumulated weights (serves the others too)."""
+    n = c_size_t()
+    _check(LIB.sparse_decode_mass_workspace_size(ctx, batch, ctypes.byref(n)), ctx)
+    return n.value
+
+
+def _check_tokens(slots, rows, names) -> int:
+    """Token rows are [T, Hkv, d], all of one shape, with one slot each."""
+    T = int(slots.numel())
+    for name, t in zip(names, rows):
+        if t.dim() != 3 or t.shape[0] != T or t.shape != rows[0].shape:
+            raise ValueError(f"{name} must be [T = {T}, Hkv, d] like {names[0]}, got {tuple(t.shape)}")
+    return T
+
+
+def _check_kv4(kv4_cache, heads: Optional[int], d: int) -> None:
+    """The records are addressed through a raw pointer: [num_pages, Hkv, page, 5 d / 4]."""
+    if kv4_cache.dim() != 4 or kv4_cache.shape[-1] != 5 * d // 4 or (heads is not None and kv4_cache.shape[1] != heads):
+        raise ValueError(f"kv4_cache must be [num_pages, Hkv, page, 5 d / 4 = {5 * d // 4}], got "
+                         f"{tuple(kv4_cache.shape)}")
+
+
+def sparse_decode_kv4_append(ctx: int, k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor,
+                             kv4_cache: torch.Tensor, stream=None) -> None:
+    """Write new tokens' keys and values ([T, Hkv, d] bf16) as 4-bit records."""
+    T = _check_tokens(slots, (k_new, v_new), ("k_new", "v_new"))
+    _check_kv4(kv4_cache, k_new.shape[1], k_new.shape[2])
+    _check(LIB.sparse_decode_kv4_append(
+        ctx, _ptr(k_new, torch.bfloat16, "k_new"), _ptr(v_new, torch.bfloat16, "v_new"),
+        _ptr(slots, torch.int32, "slots"), T, _ptr(kv4_cache, torch.uint8, "kv4_cache"),
+        _stream(stream, kv4_cache.device)), ctx)
+
+
+def sparse_decode_kv4_load(ctx: int, kv4_cache: torch.Tensor, slots: torch.Tensor, k_out: torch.Tensor,
+                           v_out: torch.Tensor, stream=None) -> None:
+    """Read tokens back from 4-bit records as bf16 [T, Hkv, d]."""
+    T = _check_tokens(slots, (k_out, v_out), ("k_out", "v_out"))
+    _check_kv4(kv4_cache, k_out.shape[1], k_out.shape[2])
+    _check(LIB.sparse_decode_kv4_load(
+        ctx, _ptr(kv4_cache, torch.uint8, "kv4_cache"), _ptr(slots, torch.int32, "slots"), T,
+        _ptr(k_out, torch.bfloat16, "k_out"), _ptr(v_out, torch.bfloat16, "v_out"),
+        _stream(stream, kv4_cache.device)), ctx)
+
+
+def sparse_decode_attend_kv4(ctx: int, q, kv4_cache, page_table, seq_lens, sel_idx, sel_count, out, workspace,
+                             mass=None, stream=None) -> None:
+    """attend on a cache of 4-bit records; with `mass`, as attend_mass."""
+    _check_sets(ctx, sel_idx, sel_count, int(seq_lens.numel()))
+    _check_kv4(kv4_cache, None, q.shape[-1])
+    stride = int(sel_idx.shape[-1]) if sel_idx is not None else 0
+    _check(LIB.sparse_decode_attend_kv4(
+        ctx, _ptr(q, torch.bfloat16, "q"), _ptr(kv4_cache, torch.uint8, "kv4_cache"),
+        _ptr(page_table, torch.int32, "page_table"), _ptr(seq_lens, torch.int32, "seq_lens"),
+        int(seq_lens.numel()), _ptr(sel_idx, torch.int32, "sel_idx"), _ptr(sel_count, torch.int32, "sel_count"),
+        stride, _ptr(out, torch.float32, "out"), _ptr(mass, torch.float32, "mass"),
+        _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream(stream, q.device)), ctx)
+
+
+def sparse_decode_select_attend_kv4(ctx: int, q_pre, q, index_cache, kv4_cache, page_table, seq_lens, sel_idx,
+                                    sel_count, out, workspace, mass=None, stream=None) -> None:
+    """select followed by attend_kv4 on the same sets, in one call."""
+    _check_sets(ctx, sel_idx, sel_count, int(seq_lens.numel()))
+    _check_kv4(kv4_cache, None, q.shape[-1])
+    stride = int(sel_idx.shape[-1]) if sel_idx is not None else 0
+    _check(LIB.sparse_decode_select_attend_kv4(
+        ctx, _ptr(q_pre, torch.bfloat16, "q_pre"), _ptr(q, torch.bfloat16, "q"),
+        _ptr(index_cache, torch.bfloat16, "index_cache"), _ptr(kv4_cache, torch.uint8, "kv4_cache"),
+        _ptr(page_table, torch.int32, "page_table"), _ptr(seq_lens, torch.int32, "seq_lens"),
+        int(seq_lens.numel()), _ptr(sel_idx, torch.int32, "sel_idx"), _ptr(sel_count, torch.int32, "sel_count"),
+        stride, _ptr(out, torch.float32, "out"), _ptr(mass, torch.float32, "mass"),
+        _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream(stream, q.device)), ctx)
+
+
+def sparse_decode_attend_mass(ctx: int, q, k_cache, v_cache, page_table, seq_lens, sel_idx, sel_count, out, mass,
+                              workspace, stream=None) -> None:
+    """attend that adds every attention weight to mass [num_pages, Hkv, page]."""
+    _check_sets(ctx, sel_idx, sel_count, int(seq_lens.numel()))
+    stride = int(sel_idx.shape[-1]) if sel_idx is not None else 0
+    _check(LIB.sparse_decode_attend_mass(
+        ctx, _ptr(q, torch.bfloat16, "q"), _ptr(k_cache, torch.bfloat16, "k_cache"),
+        _ptr(v_cache, torch.bfloat16, "v_cache"), _ptr(page_table, torch.int32, "page_table"),
+        _ptr(seq_lens, torch.int32, "seq_lens"), int(seq_lens.numel()),
+        _ptr(sel_idx, torch.int32, "sel_idx"), _ptr(sel_count, torch.int32, "sel_count"), stride,
+        _ptr(out, torch.float32, "out"), _ptr(mass, torch.float32, "mass"),
+        _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream(stream, q.device)), ctx)
+
+
+def sparse_decode_select_attend_mass(ctx: int, q_pre, q, index_cache, k_cache, v_cache, page_table, seq_lens, sel_idx,
+                                     sel_count, out, mass, workspace, stream=None) -> None:
+    """select followed by attend_mass on the same sets, in one call."""
+    _check_sets(ctx, sel_idx, sel_count, int(seq_lens.numel()))
+    stride = int(sel_idx.shape[-1]) if sel_idx is not None else 0
+    _check(LIB.sparse_decode_select_attend_mass(
+        ctx, _ptr(q_pre, torch.bfloat16, "q_pre"), _ptr(q, torch.bfloat16, "q"),
+        _ptr(index_cache, torch.bfloat16, "index_cache"), _ptr(k_cache, torch.bfloat16, "k_cache"),
+        _ptr(v_cache, torch.bfloat16, "v_cache"), _ptr(page_table, torch.int32, "page_table"),
+        _ptr(seq_lens, torch.int32, "seq_lens"), int(seq_lens.numel()),
+        _ptr(sel_idx, torch.int32, "sel_idx"), _ptr(sel_count, torch.int32, "sel_count"), stride,
+        _ptr(out, torch.float32, "out"), _ptr(mass, torch.float32, "mass"),
+        _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream(stream, q.device)), ctx)
+
+
+def sparse_decode_evict(ctx: int, mass, page_table, seq_lens, new_page_table, budget: int, keep_first: int,
+                        keep_last: int, kept, new_lens, k_cache=None, v_cache=None, index_cache=None, kv4_cache=None,
+                        stream=None) -> None:
+    """Shorten every sequence to `budget` tokens per KV head by accumulated
+    weight, moving the kept rows of the given caches to the pages of
+    new_page_table.  kept int32 [B, Hkv, budget], new_lens int32 [B]."""
+    B = int(seq_lens.numel())
+    if kept.dim() != 3 or kept.shape[0] < B or kept.shape[1] != mass.shape[1] or kept.shape[2] != budget:
+        raise ValueError(f"kept must be [B >= {B}, Hkv = {mass.shape[1]}, budget = {budget}], got {tuple(kept.shape)}")
+    if new_lens.numel() < B:
+        raise ValueError(f"new_lens must hold {B} entries, got {new_lens.numel()}")
+    if new_page_table.dim() != 2 or new_page_table.shape[0] < B or new_page_table.shape[1] != page_table.shape[1]:
+        raise ValueError(f"new_page_table must be [B >= {B}, MAXP = {page_table.shape[1]}], got "
+                         f"{tuple(new_page_table.shape)}")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("index_cache", index_cache),
+                    ("kv4_cache", kv4_cache)):
+        if t is not None and tuple(t.shape[:3]) != tuple(mass.shape):
+            raise ValueError(f"{name} must be [num_pages, Hkv, page, ...] like mass {tuple(mass.shape)}, got "
+                             f"{tuple(t.shape)}")
+    _check(LIB.sparse_decode_evict(
+        ctx, _ptr(mass, torch.float32, "mass"), _ptr(page_table, torch.int32, "page_table"),
+        _ptr(seq_lens, torch.int32, "seq_lens"), B, _ptr(new_page_table, torch.int32, "new_page_table"),
+        int(budget), int(keep_first), int(keep_last), _ptr(kept, torch.int32, "kept"),
+        _ptr(new_lens, torch.int32, "new_lens"), _ptr(k_cache, torch.bfloat16, "k_cache"),
+        _ptr(v_cache, torch.bfloat16, "v_cache"), _ptr(index_cache, torch.bfloat16, "index_cache"),
+        _ptr(kv4_cache, torch.uint8, "kv4_cache"), _stream(stream, mass.device)), ctx)
+
+
 def sparse_decode_error_word(ctx: int, stream=None) -> int:
     """Wait for the stream, read and clear the device error word (0 = clean)."""
     w = c_uint32()
@@ -399,6 +539,9 @@ class SparseDecode:
     def workspace_size(self, batch: int) -> int:
         return sparse_decode_workspace_size(self.handle, batch)
 
+    def mass_workspace_size(self, batch: int) -> int:
+        return sparse_decode_mass_workspace_size(self.handle, batch)
+
     def sel_stride(self) -> int:
         if self.cfg.get("mode", "top_p") == "top_p":
             return self.max_len
@@ -409,9 +552,11 @@ class SparseDecode:
         import numpy as np
         return min(self.max_len, max(1, math.floor(float(np.float32(self.cfg["top_k_frac"])) * self.max_len)))
 
-    def alloc(self, batch: int):
-        """Workspace, selection rows and counts for `batch` sequences."""
-        ws = torch.empty(self.workspace_size(batch), dtype=torch.uint8, device=self.device)
+    def alloc(self, batch: int, mass: bool = False):
+        """Workspace, selection rows and counts for `batch` sequences; with
+        `mass`, the workspace also serves the calls that accumulate weights."""
+        size = self.mass_workspace_size(batch) if mass else self.workspace_size(batch)
+        ws = torch.empty(size, dtype=torch.uint8, device=self.device)
         h = max(1, self.num_retrieval_heads)
         sel = torch.empty((batch, h, self.sel_stride()), dtype=torch.int32, device=self.device)
         cnt = torch.zeros((batch, h), dtype=torch.int32, device=self.device)
@@ -467,6 +612,94 @@ class SparseDecode:
         shape = (max_batch or self.cfg["max_batch"], self.num_local_groups(), rows, self.cfg["head_dim"])
         return (torch.zeros(shape, dtype=torch.bfloat16, device=self.device),
                 torch.zeros(shape, dtype=torch.bfloat16, device=self.device))
+
+    # ---- 4-bit cache, accumulated weights and eviction
+
+    def _paged(self, t, last, name):
+        """The paged caches are addressed through raw pointers: check the whole shape."""
+        want = (self.cfg["num_pages"], self.cfg["num_kv_heads"], self.cfg.get("page_size", 16)) + last
+        if t is not None and tuple(t.shape) != want:
+            raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
+
+    def _batch(self, q, page_table, seq_lens, out):
+        """q, out [B, Hq, d], page_table [B, MAXP] of a batch of seq_lens [B]."""
+        want = (int(seq_lens.numel()), self.cfg["num_q_heads"], self.cfg["head_dim"])
+        if tuple(q.shape) != want or tuple(out.shape) != want:
+            raise ValueError(f"q and out must be {want}, got {tuple(q.shape)} / {tuple(out.shape)}")
+        self._table(page_table, seq_lens, "page_table")
+
+    def _table(self, page_table, seq_lens, name):
+        if page_table.dim() != 2 or page_table.shape[0] < seq_lens.numel() or \
+                page_table.shape[1] != self.cfg["max_pages_per_seq"]:
+            raise ValueError(f"{name} must be [B >= {seq_lens.numel()}, MAXP = {self.cfg['max_pages_per_seq']}], got "
+                             f"{tuple(page_table.shape)}")
+
+    def _tokens(self, t, name):
+        if t.dim() != 3 or tuple(t.shape[1:]) != (self.cfg["num_kv_heads"], self.cfg["head_dim"]):
+            raise ValueError(f"{name} must be [T, Hkv = {self.cfg['num_kv_heads']}, d = {self.cfg['head_dim']}], got "
+                             f"{tuple(t.shape)}")
+
+    def kv4_cache(self):
+        """A zeroed cache of 4-bit records over the context's pages."""
+        shape = (self.cfg["num_pages"], self.cfg["num_kv_heads"], self.cfg.get("page_size", 16),
+                 5 * self.cfg["head_dim"] // 4)
+        return torch.zeros(shape, dtype=torch.uint8, device=self.device)
+
+    def mass_cache(self):
+        """Zeroed accumulated weights over the context's pages."""
+        shape = (self.cfg["num_pages"], self.cfg["num_kv_heads"], self.cfg.get("page_size", 16))
+        return torch.zeros(shape, dtype=torch.float32, device=self.device)
+
+    def kv4_append(self, k_new, v_new, slots, kv4_cache, stream=None):
+        self._tokens(k_new, "k_new")
+        self._paged(kv4_cache, (5 * self.cfg["head_dim"] // 4,), "kv4_cache")
+        sparse_decode_kv4_append(self.handle, k_new, v_new, slots, kv4_cache, stream)
+
+    def kv4_load(self, kv4_cache, slots, k_out, v_out, stream=None):
+        self._tokens(k_out, "k_out")
+        self._paged(kv4_cache, (5 * self.cfg["head_dim"] // 4,), "kv4_cache")
+        sparse_decode_kv4_load(self.handle, kv4_cache, slots, k_out, v_out, stream)
+
+    def attend_kv4(self, q, kv4_cache, page_table, seq_lens, sel_idx, sel_count, out, workspace, mass=None,
+                   stream=None):
+        self._batch(q, page_table, seq_lens, out)
+        self._paged(kv4_cache, (5 * self.cfg["head_dim"] // 4,), "kv4_cache")
+        self._paged(mass, (), "mass")
+        sparse_decode_attend_kv4(self.handle, q, kv4_cache, page_table, seq_lens, sel_idx, sel_count, out, workspace,
+                                 mass, stream)
+
+    def select_attend_kv4(self, q_pre, q, index_cache, kv4_cache, page_table, seq_lens, sel_idx, sel_count, out,
+                          workspace, mass=None, stream=None):
+        self._batch(q, page_table, seq_lens, out)
+        self._paged(kv4_cache, (5 * self.cfg["head_dim"] // 4,), "kv4_cache")
+        self._paged(mass, (), "mass")
+        sparse_decode_select_attend_kv4(self.handle, q_pre, q, index_cache, kv4_cache, page_table, seq_lens, sel_idx,
+                                        sel_count, out, workspace, mass, stream)
+
+    def attend_mass(self, q, k_cache, v_cache, page_table, seq_lens, sel_idx, sel_count, out, mass, workspace,
+                    stream=None):
+        self._batch(q, page_table, seq_lens, out)
+        self._paged(mass, (), "mass")
+        sparse_decode_attend_mass(self.handle, q, k_cache, v_cache, page_table, seq_lens, sel_idx, sel_count, out,
+                                  mass, workspace, stream)
+
+    def select_attend_mass(self, q_pre, q, index_cache, k_cache, v_cache, page_table, seq_lens, sel_idx, sel_count,
+                           out, mass, workspace, stream=None):
+        self._batch(q, page_table, seq_lens, out)
+        self._paged(mass, (), "mass")
+        sparse_decode_select_attend_mass(self.handle, q_pre, q, index_cache, k_cache, v_cache, page_table, seq_lens,
+                                         sel_idx, sel_count, out, mass, workspace, stream)
+
+    def evict(self, mass, page_table, seq_lens, new_page_table, budget, keep_first, keep_last, kept, new_lens,
+              k_cache=None, v_cache=None, index_cache=None, kv4_cache=None, stream=None):
+        d = self.cfg["head_dim"]
+        self._paged(mass, (), "mass")
+        self._table(page_table, seq_lens, "page_table")
+        for name, t, last in (("k_cache", k_cache, d), ("v_cache", v_cache, d), ("index_cache", index_cache, 16),
+                              ("kv4_cache", kv4_cache, 5 * d // 4)):
+            self._paged(t, (last,), name)
+        sparse_decode_evict(self.handle, mass, page_table, seq_lens, new_page_table, budget, keep_first, keep_last,
+                            kept, new_lens, k_cache, v_cache, index_cache, kv4_cache, stream)
 
     def error_word(self, stream=None) -> int:
         return sparse_decode_error_word(self.handle, stream)

@@ -39,8 +39,9 @@
  *     q and q_pre must start on a 16-byte boundary (they are read with 16-byte
  *     vector and asynchronous copies); a misaligned one is rejected with
  *     SD_ERR_INVALID_ARG.
- *   - Hot calls (index_keys, local_append, select, attend and their joined
- *     and split forms) allocate nothing, never synchronise the host, and
+ *   - Hot calls (index_keys, local_append, select, attend and their joined,
+ *     split, 4-bit and weight-accumulating forms, kv4_append, kv4_load, evict)
+ *     allocate nothing, never synchronise the host, and
  *     enqueue their work on `stream` (a cudaStream_t; NULL = the legacy
  *     default stream).  Argument errors are
  *     detected on the host before any launch and nothing is enqueued.
@@ -62,6 +63,12 @@
  *   k_cache, v_cache  bf16 [num_pages, Hkv, P, d]; token j of sequence b, KV
  *                     head g lives at [page_table[b][j / P], g, j % P, :].
  *   index_cache       bf16 [num_pages, Hkv, P, r]; same addressing.
+ *   kv4_cache         uint8 [num_pages, Hkv, P, 5 d / 4]: a 4-bit record in
+ *                     place of a k_cache and a v_cache row; same addressing
+ *                     (see sparse_decode_kv4_append).
+ *   mass              float32 [num_pages, Hkv, P]: accumulated attention
+ *                     weight of each cached row; same addressing (see
+ *                     sparse_decode_attend_mass).
  *   page_table        int32 [B, MAXP]; entries at and past ceil(N_b / P) are
  *                     never read.
  *   seq_lens          int32 [B]; N_b, 0 <= N_b <= L.  The current token is
@@ -107,7 +114,9 @@ enum {
   SD_EBIT_SEQLEN = 2u,     /* N_b < 0 or N_b > L */
   SD_EBIT_SEL = 4u,        /* sel_idx entry outside [0, N_b), not ascending, or sel_count > sel_stride */
   SD_EBIT_SLOT = 8u,       /* index_keys slot outside [0, num_pages * P) */
-  SD_EBIT_TIMEOUT = 16u    /* a bounded device-side wait gave up */
+  SD_EBIT_TIMEOUT = 16u,   /* a bounded device-side wait gave up */
+  SD_EBIT_VALUE = 32u      /* kv4_append: a group of 32 channels with a NaN, an infinity or a range
+                              beyond float32 (stored as zeros) */
 };
 
 /*
@@ -457,6 +466,161 @@ SD_API sd_status sparse_decode_attend_noalloc(sd_ctx *ctx, const void *q, const 
                                       const int32_t *seq_lens, int batch, const int32_t *sel_idx,
                                       const int32_t *sel_count, int sel_stride, float *out,
                                       sd_stream stream);
+
+/*
+ * 4-bit cache.  One record holds the key and the value of one token of one KV
+ * head in 5 d / 4 bytes (160 at d = 128, against 512 in bf16).  The d channels
+ * of each are split into NG = d / 32 groups of 32; a channel stands for
+ *
+ *   lo + s * code,   code in 0 .. 15, lo and s bf16 per group.
+ *
+ * Layout of a record (little endian):
+ *   d / 2 bytes  key codes:   the 32-bit word t * NG + g (t = 0 .. 3) holds
+ *                channels 32 g + 8 t .. + 7, the lowest in the low nibble
+ *   d / 2 bytes  value codes: the 16-bit word c * NG + g (c = 0 .. 7) holds
+ *                channels 32 g + 4 c .. + 3, the lowest in the low nibble
+ *   d / 4 bytes  bf16: key s [NG], key lo [NG], value s [NG], value lo [NG]
+ *
+ * sparse_decode_kv4_append -- write the records of `num_tokens` new tokens.
+ * Per group of 32 channels x of a key or value row:
+ *
+ *   lo   = min x                                       (exact)
+ *   s    = bf16_rne( float32( (max x - lo) / 15 ) )    (float32 operations)
+ *   code = min(15, rint((x - lo) / s))                 (ties to even, decided
+ *                                                       as in float64; 0 if s = 0)
+ *
+ *   k_new, v_new  device bf16 [num_tokens, Hkv, d], post-RoPE keys and values.
+ *   slots         device int32 [num_tokens], page * P + offset of each token.
+ *   kv4_cache     device, 16-byte aligned, written in place.
+ *
+ * A slot outside the pool sets SD_EBIT_SLOT and is skipped.  A group with a NaN
+ * or an infinity, or whose range exceeds float32, sets SD_EBIT_VALUE and is
+ * stored as zeros, so records are always finite.  The same slot twice in a call
+ * leaves an unspecified mix of the two tokens.  num_tokens == 0 is a no-op.
+ */
+SD_API sd_status sparse_decode_kv4_append(sd_ctx *ctx, const void *k_new, const void *v_new, const int32_t *slots,
+                                   int num_tokens, void *kv4_cache, sd_stream stream);
+
+/*
+ * sparse_decode_kv4_load -- read `num_tokens` tokens back as bf16:
+ *
+ *   k_out[t, g, :] = bf16_rne( float32( lo + s * code ) )  of slot slots[t]
+ *
+ * (and likewise v), for the calls that take bf16 caches (prefill of a later
+ * chunk, exact-score selection).
+ *
+ *   k_out, v_out  device bf16 [num_tokens, Hkv, d], 16-byte aligned.
+ *
+ * A slot outside the pool sets SD_EBIT_SLOT and leaves its output rows as they
+ * were.  num_tokens == 0 is a no-op.
+ */
+SD_API sd_status sparse_decode_kv4_load(sd_ctx *ctx, const void *kv4_cache, const int32_t *slots, int num_tokens,
+                                 void *k_out, void *v_out, sd_stream stream);
+
+/*
+ * sparse_decode_attend_kv4 -- sparse_decode_attend on a 4-bit cache: the keys
+ * and values are the numbers the records stand for (no rounding of their own),
+ * float32 accumulation.  Same arguments otherwise.
+ *
+ *   mass  NULL, or as for sparse_decode_attend_mass; the workspace must then
+ *         have sparse_decode_mass_workspace_size bytes.
+ *
+ * Records that no append has written may hold NaN scales; they must not be
+ * inside any head's set.
+ */
+SD_API sd_status sparse_decode_attend_kv4(sd_ctx *ctx, const void *q, const void *kv4_cache,
+                                   const int32_t *page_table, const int32_t *seq_lens, int batch,
+                                   const int32_t *sel_idx, const int32_t *sel_count, int sel_stride, float *out,
+                                   float *mass, void *workspace, size_t ws_bytes, sd_stream stream);
+
+/*
+ * sparse_decode_select_attend_kv4 -- sparse_decode_select_attend on a 4-bit
+ * cache (the index cache keeps its layout).  Arguments, results and errors as
+ * for sparse_decode_select_attend and sparse_decode_attend_kv4.
+ */
+SD_API sd_status sparse_decode_select_attend_kv4(sd_ctx *ctx, const void *q_pre, const void *q,
+                                          const void *index_cache, const void *kv4_cache,
+                                          const int32_t *page_table, const int32_t *seq_lens, int batch,
+                                          int32_t *sel_idx, int32_t *sel_count, int sel_stride, float *out,
+                                          float *mass, void *workspace, size_t ws_bytes, sd_stream stream);
+
+/*
+ * sparse_decode_attend_mass -- sparse_decode_attend that also accumulates the
+ * attention weights per cached row:
+ *
+ *   mass[page_table[b][j / P], g, j % P] += sum over the heads h of KV group g
+ *       with j in their set of  e^{l_j - max l} / sum_{j' in S} e^{l_j' - max l}
+ *
+ * Rows outside every set keep their value.  The sums are float32 and the same
+ * in every run, unless sequences of the batch share pages: their weights then
+ * all count, added in no fixed order.
+ *
+ *   mass       device float32 [num_pages, Hkv, P], updated in place.
+ *   workspace  at least sparse_decode_mass_workspace_size bytes.
+ */
+SD_API sd_status sparse_decode_attend_mass(sd_ctx *ctx, const void *q, const void *k_cache, const void *v_cache,
+                                    const int32_t *page_table, const int32_t *seq_lens, int batch,
+                                    const int32_t *sel_idx, const int32_t *sel_count, int sel_stride, float *out,
+                                    float *mass, void *workspace, size_t ws_bytes, sd_stream stream);
+
+/*
+ * sparse_decode_select_attend_mass -- sparse_decode_select_attend that also
+ * accumulates the weights.  Arguments, results and errors as for
+ * sparse_decode_select_attend and sparse_decode_attend_mass.
+ */
+SD_API sd_status sparse_decode_select_attend_mass(sd_ctx *ctx, const void *q_pre, const void *q,
+                                           const void *index_cache, const void *k_cache, const void *v_cache,
+                                           const int32_t *page_table, const int32_t *seq_lens, int batch,
+                                           int32_t *sel_idx, int32_t *sel_count, int sel_stride, float *out,
+                                           float *mass, void *workspace, size_t ws_bytes, sd_stream stream);
+
+/*
+ * sparse_decode_mass_workspace_size -- bytes of device workspace that the calls
+ * with accumulated weights need for a batch of `batch` sequences; it serves
+ * every call that takes sparse_decode_workspace_size bytes as well.
+ */
+SD_API sd_status sparse_decode_mass_workspace_size(const sd_ctx *ctx, int batch, size_t *bytes);
+
+/*
+ * sparse_decode_evict -- shorten every sequence of the batch to at most `budget`
+ * cached tokens per KV head.  Of a sequence with N_b > budget each KV head g
+ * keeps, as its own set,
+ *
+ *   positions [0, keep_first) and [N_b - keep_last, N_b), and of the others the
+ *   budget - keep_first - keep_last of highest mass, ties to the lower position;
+ *
+ * a sequence with N_b <= budget keeps all.  The kept rows, in ascending order
+ * of position, become positions 0 .. n_b - 1, n_b = min(N_b, budget), of the
+ * sequence on its new pages: for every cache given (NULL = absent) and mass,
+ *
+ *   cache[new_page_table[b][i / P], g, i % P, :] = cache[page_table[b][j_i / P], g, j_i % P, :]
+ *
+ * The old pages are only read: the caller frees them, and pages shared with
+ * other sequences stay valid for those.  With keep_first >= num_sinks and
+ * keep_last >= window the local heads' sets are unchanged.
+ *
+ *   mass            device float32 [num_pages, Hkv, P].  A NaN counts above
+ *                   every number if its sign bit is clear, below if set.
+ *   new_page_table  device int32 [B, MAXP]; entries [0, ceil(n_b / P)) name
+ *                   pages that no sequence of the batch uses, each once (rows of
+ *                   a page that is both read and written, or written twice, are
+ *                   unspecified).  Slots past n_b - 1 of the last page are left
+ *                   as they were.
+ *   kept            device int32 [B, Hkv, budget]: receives j_i; entries past
+ *                   n_b - 1 are left as they were.
+ *   new_lens        device int32 [B]: receives n_b.  Not the same memory as
+ *                   seq_lens.
+ *   k_cache, v_cache, index_cache, kv4_cache   device, 16-byte aligned, or NULL.
+ *   budget          in [1, L]; keep_first, keep_last >= 0 with
+ *                   keep_first + keep_last <= budget.
+ *
+ * No workspace.  A page id outside the pool sets SD_EBIT_PAGE and its rows are
+ * skipped.
+ */
+SD_API sd_status sparse_decode_evict(sd_ctx *ctx, float *mass, const int32_t *page_table, const int32_t *seq_lens,
+                              int batch, const int32_t *new_page_table, int budget, int keep_first, int keep_last,
+                              int32_t *kept, int32_t *new_lens, void *k_cache, void *v_cache, void *index_cache,
+                              void *kv4_cache, sd_stream stream);
 
 /*
  * sparse_decode_error_word -- wait for `stream`, copy the device error word
