@@ -4,44 +4,114 @@
 //
 // A key of group g of 32 channels is k_i = lo_g + s_g c_i, so a logit is
 //   q.k = sum_g [ s_g (sum_{i in g} q_i c_i) + lo_g (sum_{i in g} q_i) ] :
-// the tensor cores contract the bf16 query with the codes (exact in bf16), one
-// accumulator per group, and the scales join in float32.  Likewise
-//   o_i = sum_j p_j v_ji = sum_j (p_j s_jg) (c_ji - 8) + sum_j p_j (lo_jg + 8 s_jg) :
-// the B operand is p s, split into bf16 hi + lo terms (together within 2^-18 of
-// it), the A operand the codes about their middle (exact), and the second sum
-// is kept per group in float32.
+// the tensor cores contract the query with the codes, one accumulator per
+// group, and the scales join in float32.  Likewise
+//   o_i = sum_j (p_j s_jg) (c_ji - 8) + sum_j p_j (lo_jg + 8 s_jg) :
+// the operands are p s and the codes about their middle (sums of either sign:
+// the tensor cores truncate what they add to an accumulator, and a sum of
+// positive terms many times the result would lose 3e-6 of it over 16 tiles), and
+// the second sum is kept per group in float32.
+//
+// Everything is contracted in f16, where a code is two instructions away: the
+// four bits of a nibble put at bits 0-3 or 4-7 of f16's 1024 are 1024 + c or
+// 1024 + 16 c, and one addition or fused multiply-add makes them c - 8.  (The
+// bare bits, subnormal numbers, would be the codes for free, but the tensor cores
+// align products by the subnormals' nominal exponent and lose about nine bits of
+// the sums: 3e-5 of the output.)
+// The other operand takes powers of two that keep it in f16's range:
+//   q  times 2^k, its largest element in [2^14, 2^15): exact down to 2^-29 of
+//      the largest, and off by at most 2^-40 of it below;
+//   p s  times 2^-R_g, R_g per group such that the largest s of the first tile
+//      lies in [2^10, 2^11), moved only when a larger s comes along; p s is split
+//      into f16 hi + lo terms, together within 2^-22 of it (or 2^-34 of the
+//      largest), so that weights keep nearly float32 accuracy.
+// The softmax reference of a head also moves only when a logit exceeds it by
+// 2^4, so most tiles need no exchange for the maximum and no rescaling.
 //
 // Per warp, a 16-row tile (16 records):
-//   S  heads on M, rows on N (mma.m16n8k16, B = key codes straight from the
-//      record's words), so the scores leave in the layout that P V wants for B;
-//   P V channels on M (A = value codes), heads on N.  With at most four heads,
-//      columns 0-3 carry the hi terms and 4-7 the lo terms of the same heads:
-//      half the MMAs.  Column n of S is row (n >> 1) + 4 (n & 1) of its half
-//      tile, which spreads the value loads over the banks.
-// The softmax reference of a head moves only when a logit exceeds it by 2^8
-// (weights stay in float32 range and relative precision), so most tiles need no
-// exchange for the maximum and no rescaling.
+//   S    heads on M, rows on N (mma.m16n8k16, B = key codes), so the scores leave
+//        in the layout that P V wants for B;
+//   P V  channels on M (A = value codes), heads on N.  With at most four heads,
+//        columns 0-3 carry the hi terms and 4-7 the lo terms of the same heads:
+//        half the MMAs.  Column n of S is row (n >> 1) + 4 (n & 1) of its half
+//        tile, which spreads the value loads over the banks.
 #include "sd_attend.cuh"
-
-#include <cuda_bf16.h>
 
 namespace sd {
 namespace {
 
 constexpr int kRing4 = 4;               // tiles in flight per warp
-constexpr float kLazy = 8.0f;           // a head's reference may lag its maximum by this (log2)
-
-// nibble i of both 16-bit halves, as bf16: 128 + code (exact: bf16 carries 8 bits)
-__device__ __forceinline__ uint32_t nibble_pair(uint32_t w, int i) {
-  return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-}
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+constexpr float kLazy = 4.0f;           // a head's reference may lag its maximum by this (log2)
+constexpr int kScaleTop = 10;           // exponent of the largest p s at p = 1
+// the nibbles at bits 0-3 (low) and 4-7 (high) of both halves of w, as f16: code - 8
+__device__ __forceinline__ uint32_t low_codes(uint32_t w) {
   uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  asm("add.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"((w & 0x000F000Fu) | 0x64006400u), "r"(0xE408E408u));   // - 1032
   return r;
 }
-constexpr uint32_t k128x2 = 0x43004300u;   // bf16 128, twice
-constexpr uint32_t k136x2 = 0x43084308u;   // bf16 136, twice
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;\n"                          // / 16 - 72
+      : "=r"(r)
+      : "r"((w & 0x00F000F0u) | 0x64006400u), "r"(0x2C002C00u), "r"(0xD480D480u));
+  return r;
+}
+// d += a * b, f16 inputs, float32 accumulate
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// two floats -> f16x2 (x in the low half), round to nearest even
+__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(y), "f"(x));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t w) {
+  float2 r;
+  asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}\n" : "=f"(r.x), "=f"(r.y) : "r"(w));
+  return r;
+}
+// the bf16 halves (hi = 0: low, 1: high) of two words
+__device__ __forceinline__ float2 halves(uint32_t a, uint32_t b, int hi) {
+  return hi ? make_float2(bf16_hi(a), bf16_hi(b)) : make_float2(bf16_lo(a), bf16_lo(b));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};"
+      " fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d;}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// either half of a greater than that of b (or not a number)
+__device__ __forceinline__ bool any_gt_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{.reg .pred p, q; setp.gtu.bf16x2 p|q, %1, %2; or.pred p, p, q; selp.u32 %0, 1, 0, p;}\n" : "=r"(r) : "r"(a), "r"(b));
+  return r != 0u;
+}
+// 2^e for e in [-126, 127], and floor(log2) of a positive normal number
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
 
 // dynamic shared memory: [ring: kWarps x kRing4 tiles: key codes [16][d / 2] in
 //                         column order, value codes [16][d / 2], scales [16][d / 4]]
@@ -56,8 +126,6 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
   constexpr int kHalf = D / 2;                       // bytes of a row's key (or value) codes
   constexpr int kMeta = D / 4;                       // bytes of a row's scales
   constexpr int kTileB = kTileRows * kRec;
-  constexpr int CPR = kRec / 16;                     // 16-byte chunks per record
-  constexpr int CPL = (kTileRows * CPR + 31) / 32;   // chunks per lane and tile
   constexpr bool PACK = GR <= 4;                     // hi and lo terms side by side on N
   constexpr int HB = GR > 8 ? 2 : 1;                 // column blocks of heads
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -82,25 +150,19 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
     if (lane == 0) S.item = i;
   }
 
-  // copies: chunk x = lane + 32 j of a tile is chunk x % CPR of row x / CPR
-  // (whole records, coalesced); where it goes in the tile
-  uint32_t cdst[CPL];
-#pragma unroll
-  for (int j = 0; j < CPL; ++j) {
-    const int x = lane + 32 * j, r = x / CPR, ch = x % CPR;
-    const int col = (r & 8) + 2 * (r & 3) + ((r >> 2) & 1);       // column of row r
-    if (ch < kHalf / 16)
-      cdst[j] = col * kHalf + ch * 16;
-    else if (ch < 2 * (kHalf / 16))
-      // d = 128: rows of a bank phase differ in bits 0 and 1, four chunks each
-      cdst[j] = kTileRows * kHalf + r * kHalf + (((ch - kHalf / 16) ^ (D == 128 ? 2 * ((r >> 1) & 1) : 0)) * 16);
-    else
-      cdst[j] = 2 * kTileRows * kHalf + r * kMeta + (ch - 2 * (kHalf / 16)) * 16;
-  }
+  // copies: lanes 2 r and 2 r + 1 take row r of a tile, the even and the odd
+  // 16-byte chunks (whole sectors); where they go in the tile
+  const int crow = lane >> 1, odd = lane & 1;
+  const int ccol = (crow & 8) + 2 * (crow & 3) + ((crow >> 2) & 1);             // column of the row
+  const int cplace = 4 * (crow & 3) + 2 * (crow >> 3) + ((crow >> 2) & 1);      // its place among the fragments
+  const int swz = D == 128 ? 32 * ((crow >> 1) & 1) : 0;   // d = 128: rows of a bank phase differ in bits 0 and 1
+  const uint32_t kdst = ccol * kHalf + 16 * odd;
+  const uint32_t vdst = kTileRows * kHalf + crow * kHalf + 16 * odd;
+  const uint32_t mdst = 2 * kTileRows * kHalf + crow * kMeta + 16 * odd;
   const float sc = a.attn_scale * kLog2e;
   const uint64_t l2_stream = evict_first_policy();
   const bool is_lo = PACK && gq >= 4;
-  const float lo_mul = is_lo ? -1.0f : 0.0f;
+  const float2 lo_mul = is_lo ? make_float2(-1.0f, -1.0f) : make_float2(0.0f, 0.0f);
   const int hd = PACK ? (gq & 3) : gq;               // head (of column block 0) whose scores this lane holds
 
   long long t = t0;
@@ -151,37 +213,57 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
 
     // ---- queries: A fragments (heads on M; k = the channels of the record's
     // words: lane tq holds channels 8 tq .. 8 tq + 7 of every group, nibble pairs
-    // (i, i + 4)), and the sums over the groups' channels
+    // (i, i + 4)), and the sums over the groups' channels; all times 2^k
     uint32_t qa[NG][2][HB][2];
-    float qs[NG][HB];
+    float qs[HB][NG], qsc[HB];
 #pragma unroll
     for (int hb = 0; hb < HB; ++hb) {
       const int h = hd + 8 * hb;
       const uint16_t *qr = h < nh ? a.q + ((long long)b * sh.Hq + S.grp.q_head[h]) * D : nullptr;
+      uint4 w[NG];
+      float top = 0.0f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (qr) w = *reinterpret_cast<const uint4 *>(qr + g * kKv4Group + 8 * tq);
+        w[g] = make_uint4(0u, 0u, 0u, 0u);
+        if (qr) w[g] = *reinterpret_cast<const uint4 *>(qr + g * kKv4Group + 8 * tq);
+        const uint32_t u[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(u[i])), fabsf(bf16_hi(u[i]))));
+      }
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+      const int k = std::min(90, std::max(-90, 14 - exponent_of(top)));
+      const float f = pow2i(k);
+      qsc[hb] = sc * pow2i(-k);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
         // channels (0,1) (2,3) (4,5) (6,7) -> (0,4) (1,5) (2,6) (3,7)
-        qa[g][0][hb][0] = __byte_perm(w.x, w.z, 0x5410);
-        qa[g][0][hb][1] = __byte_perm(w.x, w.z, 0x7632);
-        qa[g][1][hb][0] = __byte_perm(w.y, w.w, 0x5410);
-        qa[g][1][hb][1] = __byte_perm(w.y, w.w, 0x7632);
-        float sum = ((bf16_lo(w.x) + bf16_hi(w.x)) + (bf16_lo(w.y) + bf16_hi(w.y))) +
-                    ((bf16_lo(w.z) + bf16_hi(w.z)) + (bf16_lo(w.w) + bf16_hi(w.w)));
+        qa[g][0][hb][0] = pack_f16(bf16_lo(w[g].x) * f, bf16_lo(w[g].z) * f);
+        qa[g][0][hb][1] = pack_f16(bf16_hi(w[g].x) * f, bf16_hi(w[g].z) * f);
+        qa[g][1][hb][0] = pack_f16(bf16_lo(w[g].y) * f, bf16_lo(w[g].w) * f);
+        qa[g][1][hb][1] = pack_f16(bf16_hi(w[g].y) * f, bf16_hi(w[g].w) * f);
+        float sum = ((bf16_lo(w[g].x) + bf16_hi(w[g].x)) + (bf16_lo(w[g].y) + bf16_hi(w[g].y))) +
+                    ((bf16_lo(w[g].z) + bf16_hi(w[g].z)) + (bf16_lo(w[g].w) + bf16_hi(w[g].w)));
         sum += __shfl_xor_sync(kFull, sum, 1);
         sum += __shfl_xor_sync(kFull, sum, 2);
-        qs[g][hb] = sum;
+        qs[hb][g] = sum * f;
       }
     }
-    float m[HB], l[HB], olo[HB][NG], o[HB][NG][2][4];
+    float m[HB], l[HB], o[HB][NG][2][4];
+    float2 olo[HB][NG];                                // two partial sums each
+    uint32_t nf[NG / 2], thr[NG / 2];                  // bf16 pairs: 2^-R_g, and the largest s it serves
+#pragma unroll
+    for (int w = 0; w < NG / 2; ++w) {
+      nf[w] = 0x3F803F80u;
+      thr[w] = 0u;
+    }
 #pragma unroll
     for (int hb = 0; hb < HB; ++hb) {
       m[hb] = -INFINITY;
       l[hb] = 0.0f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        olo[hb][g] = 0.0f;
+        olo[hb][g] = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) o[hb][g][mt][0] = o[hb][g][mt][1] = o[hb][g][mt][2] = o[hb][g][mt][3] = 0.0f;
       }
@@ -194,20 +276,16 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
     const uint32_t *prow = ws.plan_row + slot0 * ap.span;
     const uint16_t *pmask = ws.plan_mask + slot0 * ap.span;
     const int32_t *pt = a.page_table + (long long)b * sh.max_pages;
-    // lane r < 16: cache row and head mask of row r of tile q
+    int sp = 0;                                        // span of the last row fetched (rows only ascend)
+    // cache row and head mask of row lane >> 1 of tile q
     auto fetch = [&](int q, uint32_t &row, uint32_t &mask) {
       row = 0u;
       mask = 0u;
-      const int gx = r0 + (warp + q * kWarps) * kTileRows + (lane & 15);
+      const int gx = r0 + (warp + q * kWarps) * kTileRows + crow;
       if (gx >= r1) return;
       if (is_ret) {
-        int lo = 0, hi = ns_item;                      // last span s with pre[s] <= gx
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (pre[mid] <= gx) lo = mid;
-          else hi = mid;
-        }
-        const int e = lo * ap.span + (gx - pre[lo]);
+        while (pre[sp + 1] <= gx) ++sp;                // ends: gx < rows of the item = pre[ns_item]
+        const int e = sp * ap.span + (gx - pre[sp]);
         row = __ldcg(prow + e);
         mask = __ldcg(pmask + e);
       } else {
@@ -225,46 +303,45 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
       if (q < mt_w) {
         const int tile = warp + q * kWarps;
         const uint32_t row0 = __shfl_sync(kFull, row, 0);
-        if (r0 + tile * kTileRows + (lane & 15) >= r1) row = row0;
-        if (lane < kTileRows) {
-          const int x = 4 * (lane & 3) + 2 * (lane >> 3) + ((lane >> 2) & 1);   // row's place among the fragments
-          wmask[(q % kRing4) * kTileRows + x] = (uint16_t)mask;
-          if constexpr (MASS) ws.tile_row[(t + tile) * kTileRows + x] = mask ? row : kNoRow;
+        if (r0 + tile * kTileRows + crow >= r1) row = row0;
+        if (!odd) {
+          wmask[(q % kRing4) * kTileRows + cplace] = (uint16_t)mask;
+          if constexpr (MASS) ws.tile_row[(t + tile) * kTileRows + cplace] = mask ? row : kNoRow;
         }
         if constexpr (MASS)
           if (lane == 0) ws.tile_item[t + tile] = item;
         const uint32_t dst = ring_s + (q % kRing4) * kTileB;
+        const uint8_t *src = a.kv4 + (size_t)row * kRec + 16 * odd;
 #pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-          const int x = lane + 32 * j;
-          const uint32_t rj = __shfl_sync(kFull, row, (x / CPR) & 15);
-          if (x < kTileRows * CPR) cp_async16(dst + cdst[j], a.kv4 + (size_t)rj * kRec + (x % CPR) * 16, 16, l2_stream);
+        for (int j = 0; j < kHalf / 32; ++j) {
+          cp_async16(dst + kdst + 32 * j, src + 32 * j, 16, l2_stream);
+          cp_async16(dst + vdst + ((32 * j) ^ swz), src + kHalf + 32 * j, 16, l2_stream);
         }
+        if (kMeta == 32 || !odd) cp_async16(dst + mdst, src + 2 * kHalf, 16, l2_stream);
       }
       cp_async_commit();
     };
     uint32_t nrow, nmask;
-    fetch(0, nrow, nmask);
+    {
+      uint32_t rows0[kRing4], masks0[kRing4];
 #pragma unroll
-    for (int q = 0; q < kRing4; ++q) {
-      const uint32_t row = nrow, mask = nmask;
-      fetch(q + 1, nrow, nmask);
-      issue(q, row, mask);
+      for (int q = 0; q < kRing4; ++q) fetch(q, rows0[q], masks0[q]);
+      fetch(kRing4, nrow, nmask);
+#pragma unroll
+      for (int q = 0; q < kRing4; ++q) issue(q, rows0[q], masks0[q]);
     }
     for (int q = 0; q < mt_w; ++q) {
       cp_async_wait<kRing4 - 1>();                     // tile q
       __syncwarp();
       const unsigned char *kt = ring + (q % kRing4) * kTileB;
       const unsigned char *vt = kt + kTileRows * kHalf;
-      const unsigned char *mtb = vt + kTileRows * kHalf;
+      const unsigned char *mtb = vt + kTileRows * kHalf + tq * kMeta;   // scales of row tq; rows 4 (2 j + e) further on
 
       // ---- S: column n of half tile j is row 8 j + (n >> 1) + 4 (n & 1) -----------
-      float x[HB][2][2];                               // [block][half tile][e]: head, row 8 j + 4 e + tq
-#pragma unroll
-      for (int hb = 0; hb < HB; ++hb) x[hb][0][0] = x[hb][0][1] = x[hb][1][0] = x[hb][1][1] = 0.0f;
+      float2 x[HB][2];                                 // [block][half tile j], .x / .y = e: head, row 8 j + 4 e + tq
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        uint32_t kw[NG];
+        uint32_t kw[NG], mk[2][NG];                    // words; the two rows' scales and minima, bf16 pairs
         if constexpr (NG == 4) {
           const uint4 v = *reinterpret_cast<const uint4 *>(kt + (8 * j + gq) * kHalf + 16 * tq);
           kw[0] = v.x; kw[1] = v.y; kw[2] = v.z; kw[3] = v.w;
@@ -272,61 +349,106 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
           const uint2 v = *reinterpret_cast<const uint2 *>(kt + (8 * j + gq) * kHalf + 8 * tq);
           kw[0] = v.x; kw[1] = v.y;
         }
-        uint32_t ms[2][NG];                            // the two rows' scales and minima, bf16 pairs
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const unsigned char *p = mtb + (8 * j + 4 * e + tq) * kMeta;
+          const unsigned char *p = mtb + (8 * j + 4 * e) * kMeta;
           if constexpr (NG == 4) {
             const uint4 v = *reinterpret_cast<const uint4 *>(p);
-            ms[e][0] = v.x; ms[e][1] = v.y; ms[e][2] = v.z; ms[e][3] = v.w;
+            mk[e][0] = v.x; mk[e][1] = v.y; mk[e][2] = v.z; mk[e][3] = v.w;
           } else {
             const uint2 v = *reinterpret_cast<const uint2 *>(p);
-            ms[e][0] = v.x; ms[e][1] = v.y;
+            mk[e][0] = v.x; mk[e][1] = v.y;
           }
         }
 #pragma unroll
+        for (int hb = 0; hb < HB; ++hb) x[hb][j] = make_float2(0.0f, 0.0f);
+#pragma unroll
         for (int g = 0; g < NG; ++g) {
-          float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            const uint32_t b0 = sub_bf16x2(nibble_pair(kw[g], 2 * ks), k128x2);
-            const uint32_t b1 = sub_bf16x2(nibble_pair(kw[g], 2 * ks + 1), k128x2);
-            if constexpr (HB == 2)
-              mma_bf16(s, qa[g][ks][0][0], qa[g][ks][1][0], qa[g][ks][0][1], qa[g][ks][1][1], b0, b1);
-            else
-              mma_bf16(s, qa[g][ks][0][0], 0u, qa[g][ks][0][1], 0u, b0, b1);
+          // codes about 8: the accumulators start at 8 times the channels' sum
+          const float q0 = 8.0f * qs[0][g], q1 = HB == 2 ? 8.0f * qs[HB - 1][g] : 0.0f;
+          float s[4] = {q0, q0, q1, q1};
+          const uint32_t w8 = kw[g] >> 8;
+          const uint32_t b0 = low_codes(kw[g]), b1 = high_codes(kw[g]), b2 = low_codes(w8), b3 = high_codes(w8);
+          if constexpr (HB == 2) {
+            mma_f16(s, qa[g][0][0][0], qa[g][0][1][0], qa[g][0][0][1], qa[g][0][1][1], b0, b1);
+            mma_f16(s, qa[g][1][0][0], qa[g][1][1][0], qa[g][1][0][1], qa[g][1][1][1], b2, b3);
+          } else {
+            mma_f16(s, qa[g][0][0][0], 0u, qa[g][0][0][1], 0u, b0, b1);
+            mma_f16(s, qa[g][1][0][0], 0u, qa[g][1][0][1], 0u, b2, b3);
           }
+          const float2 sg = halves(mk[0][g / 2], mk[1][g / 2], g & 1);
+          const float2 lg = halves(mk[0][NG / 2 + g / 2], mk[1][NG / 2 + g / 2], g & 1);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float sg = (g & 1) ? bf16_hi(ms[e][g / 2]) : bf16_lo(ms[e][g / 2]);
-            const float lg = (g & 1) ? bf16_hi(ms[e][NG / 2 + g / 2]) : bf16_lo(ms[e][NG / 2 + g / 2]);
-#pragma unroll
-            for (int hb = 0; hb < HB; ++hb) x[hb][j][e] = fmaf(sg, s[2 * hb + e], fmaf(lg, qs[g][hb], x[hb][j][e]));
-          }
+          for (int hb = 0; hb < HB; ++hb)
+            x[hb][j] = fma2(sg, make_float2(s[2 * hb], s[2 * hb + 1]),
+                            fma2(lg, make_float2(qs[hb][g], qs[hb][g]), x[hb][j]));
         }
       }
 
-      // ---- masks and softmax -------------------------------------------------------
+      // ---- values' scales, masks and softmax ------------------------------------------
+      uint32_t vs[2][2][NG / 2], vl[2][2][NG / 2];     // [half tile][e]: scales and minima, bf16 pairs
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const unsigned char *p = mtb + (8 * j + 4 * e) * kMeta + kMeta / 2;
+          if constexpr (NG == 4) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+            vs[j][e][0] = u.x; vs[j][e][1] = u.y; vl[j][e][0] = u.z; vl[j][e][1] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            vs[j][e][0] = u.x; vl[j][e][0] = u.y;
+          }
+        }
       const uint2 mk = *reinterpret_cast<const uint2 *>(wmask + (q % kRing4) * kTileRows + 4 * tq);
       bool over = false;
+      uint32_t smax[NG / 2];
+#pragma unroll
+      for (int w = 0; w < NG / 2; ++w) {
+        smax[w] = max_bf16x2(max_bf16x2(vs[0][0][w], vs[0][1][w]), max_bf16x2(vs[1][0][w], vs[1][1][w]));
+        over |= any_gt_bf16x2(smax[w], thr[w]);
+      }
 #pragma unroll
       for (int hb = 0; hb < HB; ++hb) {
         const uint32_t bit = 1u << (hd + 8 * hb);
-        x[hb][0][0] = (mk.x & bit) ? x[hb][0][0] * sc : -INFINITY;
-        x[hb][0][1] = (mk.x & (bit << 16)) ? x[hb][0][1] * sc : -INFINITY;
-        x[hb][1][0] = (mk.y & bit) ? x[hb][1][0] * sc : -INFINITY;
-        x[hb][1][1] = (mk.y & (bit << 16)) ? x[hb][1][1] * sc : -INFINITY;
+        x[hb][0].x = (mk.x & bit) ? x[hb][0].x * qsc[hb] : -INFINITY;
+        x[hb][0].y = (mk.x & (bit << 16)) ? x[hb][0].y * qsc[hb] : -INFINITY;
+        x[hb][1].x = (mk.y & bit) ? x[hb][1].x * qsc[hb] : -INFINITY;
+        x[hb][1].y = (mk.y & (bit << 16)) ? x[hb][1].y * qsc[hb] : -INFINITY;
         if constexpr (MASS)
           if (hd + 8 * hb < nh && !is_lo)
             *reinterpret_cast<float4 *>(ws.logits + ((t + warp + (long long)q * kWarps) * gr + hd + 8 * hb) * kTileRows +
-                                        4 * tq) = make_float4(x[hb][0][0], x[hb][0][1], x[hb][1][0], x[hb][1][1]);
-        const float top = fmaxf(fmaxf(x[hb][0][0], x[hb][0][1]), fmaxf(x[hb][1][0], x[hb][1][1]));
-        over |= top > m[hb] + kLazy;
+                                        4 * tq) = make_float4(x[hb][0].x, x[hb][0].y, x[hb][1].x, x[hb][1].y);
+        over |= fmaxf(fmaxf(x[hb][0].x, x[hb][0].y), fmaxf(x[hb][1].x, x[hb][1].y)) > m[hb] + kLazy;
       }
       if (__any_sync(kFull, over)) {
+        // move the references: of every head to its maximum so far, of a group's
+        // scales where one outgrew it
+        float2 rf[NG / 2];                             // 2^(old R - new R) of the groups of a pair
+#pragma unroll
+        for (int w = 0; w < NG / 2; ++w) {
+          uint32_t top = max_bf16x2(smax[w], __shfl_xor_sync(kFull, smax[w], 1));
+          top = max_bf16x2(top, __shfl_xor_sync(kFull, top, 2));
+          float *r = reinterpret_cast<float *>(&rf[w]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float sv = i ? bf16_hi(top) : bf16_lo(top), lim = i ? bf16_hi(thr[w]) : bf16_lo(thr[w]);
+            const float old = i ? bf16_hi(nf[w]) : bf16_lo(nf[w]);
+            r[i] = 1.0f;
+            if (sv > lim) {
+              const int e = std::min(110, std::max(-110, exponent_of(sv)));
+              const float nn = pow2i(kScaleTop - e), nl = pow2i(e + 1);   // s 2^-R in [2^10, 2^11); serves up to 2^(e + 1)
+              r[i] = lim > 0.0f ? nn / old : 1.0f;     // powers of two: exact
+              const uint32_t keep = i ? 0x0000FFFFu : 0xFFFF0000u;
+              const uint32_t nb = __float_as_uint(nn) >> 16, lb = __float_as_uint(nl) >> 16;
+              nf[w] = (nf[w] & keep) | (i ? nb << 16 : nb);
+              thr[w] = (thr[w] & keep) | (i ? lb << 16 : lb);
+            }
+          }
+        }
 #pragma unroll
         for (int hb = 0; hb < HB; ++hb) {
-          float top = fmaxf(fmaxf(x[hb][0][0], x[hb][0][1]), fmaxf(x[hb][1][0], x[hb][1][1]));
+          float top = fmaxf(fmaxf(x[hb][0].x, x[hb][0].y), fmaxf(x[hb][1].x, x[hb][1].y));
           top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
           top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
           const float mn = fmaxf(m[hb], top);
@@ -336,84 +458,81 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
           const float a0 = __shfl_sync(kFull, al, 8 * tq), a1 = __shfl_sync(kFull, al, 8 * tq + 4);   // columns 2 tq, 2 tq + 1
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
-            olo[hb][g] *= al;
+            olo[hb][g] = mul2(olo[hb][g], make_float2(al, al));
+            const float r = (g & 1) ? rf[g / 2].y : rf[g / 2].x;
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
-              o[hb][g][mt][0] *= a0;
-              o[hb][g][mt][1] *= a1;
-              o[hb][g][mt][2] *= a0;
-              o[hb][g][mt][3] *= a1;
+              o[hb][g][mt][0] *= a0 * r;
+              o[hb][g][mt][1] *= a1 * r;
+              o[hb][g][mt][2] *= a0 * r;
+              o[hb][g][mt][3] *= a1 * r;
             }
           }
         }
       }
-      float p[HB][2][2];
 #pragma unroll
       for (int hb = 0; hb < HB; ++hb) {
         const float mu = m[hb] == -INFINITY ? 0.0f : m[hb];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) p[hb][j][e] = fast_exp2(x[hb][j][e] - mu);
-        l[hb] += (p[hb][0][0] + p[hb][0][1]) + (p[hb][1][0] + p[hb][1][1]);
+        for (int j = 0; j < 2; ++j) {
+          x[hb][j].x = fast_exp2(x[hb][j].x - mu);
+          x[hb][j].y = fast_exp2(x[hb][j].y - mu);
+        }
+        l[hb] += (x[hb][0].x + x[hb][0].y) + (x[hb][1].x + x[hb][1].y);
       }
 
       // ---- P V -----------------------------------------------------------------------
       uint32_t vw[2][2][NG / 2];                       // [half tile][e]: half-word pairs of groups (0,1), (2,3)
-      uint32_t ms[2][2][NG];
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = 8 * j + 4 * e + tq;
-          const unsigned char *pm = mtb + r * kMeta + kMeta / 2;
+          const unsigned char *p = vt + (8 * j + 4 * e + tq) * kHalf;
           if constexpr (NG == 4) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(vt + r * kHalf + (((gq >> 1) ^ (2 * ((tq >> 1) & 1))) * 16) +
-                                                             8 * (gq & 1));
+            const uint2 v = *reinterpret_cast<const uint2 *>(p + (((gq >> 1) ^ (tq & 2)) * 16) + 8 * (gq & 1));
             vw[j][e][0] = v.x; vw[j][e][1] = v.y;
-            const uint4 u = *reinterpret_cast<const uint4 *>(pm);
-            ms[j][e][0] = u.x; ms[j][e][1] = u.y; ms[j][e][2] = u.z; ms[j][e][3] = u.w;
           } else {
-            vw[j][e][0] = *reinterpret_cast<const uint32_t *>(vt + r * kHalf + 4 * gq);
-            const uint2 u = *reinterpret_cast<const uint2 *>(pm);
-            ms[j][e][0] = u.x; ms[j][e][1] = u.y;
+            vw[j][e][0] = *reinterpret_cast<const uint32_t *>(p + 4 * gq);
           }
         }
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        uint32_t A[2][4];                              // [m-tile]: rows gq, gq + 8 = nibbles 2 mt, 2 mt + 1
-        const uint32_t xj0 = __byte_perm(vw[0][0][g / 2], vw[0][1][g / 2], (g & 1) ? 0x7632 : 0x5410);
-        const uint32_t xj1 = __byte_perm(vw[1][0][g / 2], vw[1][1][g / 2], (g & 1) ? 0x7632 : 0x5410);
+      for (int w = 0; w < NG / 2; ++w) {
+        uint32_t vn[2][2];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          A[mt][0] = sub_bf16x2(nibble_pair(xj0, 2 * mt), k136x2);
-          A[mt][1] = sub_bf16x2(nibble_pair(xj0, 2 * mt + 1), k136x2);
-          A[mt][2] = sub_bf16x2(nibble_pair(xj1, 2 * mt), k136x2);
-          A[mt][3] = sub_bf16x2(nibble_pair(xj1, 2 * mt + 1), k136x2);
-        }
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int hb = 0; hb < HB; ++hb) {
-          uint32_t bh[2], bl[2];
+          for (int e = 0; e < 2; ++e) vn[j][e] = mul_bf16x2(vs[j][e][w], nf[w]);   // times 2^-R: exact
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float ps[2];
+        for (int i = 0; i < 2; ++i) {
+          const int g = 2 * w + i;
+          const uint32_t x0 = __byte_perm(vw[0][0][w], vw[0][1][w], i ? 0x7632 : 0x5410);
+          const uint32_t x1 = __byte_perm(vw[1][0][w], vw[1][1][w], i ? 0x7632 : 0x5410);
+          // rows gq and gq + 8 of m-tile mt: nibbles 2 mt and 2 mt + 1
+          const uint32_t A[2][4] = {{low_codes(x0), high_codes(x0), low_codes(x1), high_codes(x1)},
+                                    {low_codes(x0 >> 8), high_codes(x0 >> 8), low_codes(x1 >> 8), high_codes(x1 >> 8)}};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float sg = (g & 1) ? bf16_hi(ms[j][e][g / 2]) : bf16_lo(ms[j][e][g / 2]);
-              const float lg = (g & 1) ? bf16_hi(ms[j][e][NG / 2 + g / 2]) : bf16_lo(ms[j][e][NG / 2 + g / 2]);
-              ps[e] = p[hb][j][e] * sg;
-              olo[hb][g] = fmaf(8.0f, ps[e], fmaf(p[hb][j][e], lg, olo[hb][g]));
+          for (int hb = 0; hb < HB; ++hb) {
+            uint32_t bh[2], bl[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float2 ps = mul2(x[hb][j], halves(vn[j][0], vn[j][1], i));
+              const float2 mid = fma2(halves(vs[j][0][w], vs[j][1][w], i), make_float2(8.0f, 8.0f),
+                                      halves(vl[j][0][w], vl[j][1][w], i));
+              olo[hb][g] = fma2(x[hb][j], mid, olo[hb][g]);
+              bh[j] = pack_f16(ps.x, ps.y);
+              const float2 h = unpack_f16(bh[j]);
+              if constexpr (PACK) {                    // lanes of the lo columns: what hi left over
+                const float2 r = fma2(lo_mul, h, ps);
+                bh[j] = pack_f16(r.x, r.y);
+              } else {
+                bl[j] = pack_f16(ps.x - h.x, ps.y - h.y);
+              }
             }
-            bh[j] = pack_bf16(ps[0], ps[1]);
-            if constexpr (PACK)                        // lanes of the lo columns: what hi left over
-              bh[j] = pack_bf16(fmaf(lo_mul, bf16_lo(bh[j]), ps[0]), fmaf(lo_mul, bf16_hi(bh[j]), ps[1]));
-            else
-              bl[j] = pack_bf16(ps[0] - bf16_lo(bh[j]), ps[1] - bf16_hi(bh[j]));
-          }
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            mma_bf16(o[hb][g][mt], A[mt][0], A[mt][1], A[mt][2], A[mt][3], bh[0], bh[1]);
-            if constexpr (!PACK) mma_bf16(o[hb][g][mt], A[mt][0], A[mt][1], A[mt][2], A[mt][3], bl[0], bl[1]);
+            for (int mt = 0; mt < 2; ++mt) {
+              mma_f16(o[hb][g][mt], A[mt][0], A[mt][1], A[mt][2], A[mt][3], bh[0], bh[1]);
+              if constexpr (!PACK) mma_f16(o[hb][g][mt], A[mt][0], A[mt][1], A[mt][2], A[mt][3], bl[0], bl[1]);
+            }
           }
         }
       }
@@ -431,8 +550,9 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
       l[hb] += __shfl_xor_sync(kFull, l[hb], 2);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        olo[hb][g] += __shfl_xor_sync(kFull, olo[hb][g], 1);
-        olo[hb][g] += __shfl_xor_sync(kFull, olo[hb][g], 2);
+        float z = olo[hb][g].x + olo[hb][g].y;
+        z += __shfl_xor_sync(kFull, z, 1);
+        olo[hb][g].x = z + __shfl_xor_sync(kFull, z, 2);
       }
     }
     __syncthreads();                                   // ring no longer read
@@ -447,7 +567,8 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
       }
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        const float z0 = __shfl_sync(kFull, olo[hb][g], 8 * tq), z1 = __shfl_sync(kFull, olo[hb][g], 8 * tq + 4);
+        const float z0 = __shfl_sync(kFull, olo[hb][g].x, 8 * tq), z1 = __shfl_sync(kFull, olo[hb][g].x, 8 * tq + 4);
+        const float un = 1.0f / ((g & 1) ? bf16_hi(nf[g / 2]) : bf16_lo(nf[g / 2]));   // 2^R: exact
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           float v[4];
@@ -458,8 +579,8 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
           }
           if (!PACK || tq < 2) {
             float *d0 = cacc + (warp * GR + 8 * hb + 2 * tq) * D + g * kKv4Group + 4 * gq + 2 * mt;
-            *reinterpret_cast<float2 *>(d0) = make_float2(v[0] + z0, v[2] + z0);
-            *reinterpret_cast<float2 *>(d0 + D) = make_float2(v[1] + z1, v[3] + z1);
+            *reinterpret_cast<float2 *>(d0) = make_float2(fmaf(v[0], un, z0), fmaf(v[2], un, z0));
+            *reinterpret_cast<float2 *>(d0 + D) = make_float2(fmaf(v[1], un, z1), fmaf(v[3], un, z1));
           }
         }
       }
