@@ -117,7 +117,7 @@ sd_status attend_impl(sd_ctx *ctx, const void *q_pre, const void *q, const void 
   if (form.kv4 && !form.records) return fail(ctx, SD_ERR_INVALID_ARG, "null pointer");
   if (form.kv4 && !aligned16(form.records))
     return fail(ctx, SD_ERR_INVALID_ARG, "kv4_cache must be 16-byte aligned");
-  if (reinterpret_cast<uintptr_t>(form.mass) & 3u) return fail(ctx, SD_ERR_INVALID_ARG, "mass must be 4-byte aligned");
+  if (!aligned16(form.mass)) return fail(ctx, SD_ERR_INVALID_ARG, "mass must be 16-byte aligned");
   // local cache rows are addressed with 32-bit row numbers inside the kernels
   if (need_local && (long long)batch * ctx->tb.n_loc * local_rows(ctx) >= 0xFFFFFFFFLL)
     return fail(ctx, SD_ERR_UNSUPPORTED, "local caches too large for 32-bit row numbers");
@@ -591,6 +591,8 @@ sd_status sparse_decode_kv4_append(sd_ctx *ctx, const void *k_new, const void *v
     if (!ctx) return SD_ERR_INVALID_ARG;
     if (num_tokens < 0) return fail(ctx, SD_ERR_INVALID_ARG, "num_tokens < 0");
     if (num_tokens == 0) return SD_OK;
+    if ((long long)num_tokens * ctx->sh.Hkv >= (1LL << 31))
+      return fail(ctx, SD_ERR_UNSUPPORTED, "num_tokens * Hkv reaches 2^31");
     if (!k_new || !v_new || !slots || !kv4_cache) return fail(ctx, SD_ERR_INVALID_ARG, "null pointer");
     if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(kv4_cache))
       return fail(ctx, SD_ERR_INVALID_ARG, "k_new, v_new and kv4_cache must be 16-byte aligned");
@@ -610,6 +612,8 @@ sd_status sparse_decode_kv4_load(sd_ctx *ctx, const void *kv4_cache, const int32
     if (!ctx) return SD_ERR_INVALID_ARG;
     if (num_tokens < 0) return fail(ctx, SD_ERR_INVALID_ARG, "num_tokens < 0");
     if (num_tokens == 0) return SD_OK;
+    if ((long long)num_tokens * ctx->sh.Hkv >= (1LL << 31))
+      return fail(ctx, SD_ERR_UNSUPPORTED, "num_tokens * Hkv reaches 2^31");
     if (!kv4_cache || !slots || !k_out || !v_out) return fail(ctx, SD_ERR_INVALID_ARG, "null pointer");
     if (!aligned16(kv4_cache) || !aligned16(k_out) || !aligned16(v_out))
       return fail(ctx, SD_ERR_INVALID_ARG, "kv4_cache, k_out and v_out must be 16-byte aligned");
@@ -705,7 +709,7 @@ sd_status sparse_decode_evict(sd_ctx *ctx, float *mass, const int32_t *page_tabl
       return fail(ctx, SD_ERR_INVALID_ARG, "the new pages and lengths must not be the old ones");
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(index_cache) || !aligned16(kv4_cache))
       return fail(ctx, SD_ERR_INVALID_ARG, "the caches must be 16-byte aligned");
-    if (reinterpret_cast<uintptr_t>(mass) & 3u) return fail(ctx, SD_ERR_INVALID_ARG, "mass must be 4-byte aligned");
+    if (!aligned16(mass)) return fail(ctx, SD_ERR_INVALID_ARG, "mass must be 16-byte aligned");
     DeviceGuard dg(ctx->device);
     const int d = ctx->sh.d;
     sd::EvictArgs a{};
@@ -721,10 +725,11 @@ sd_status sparse_decode_evict(sd_ctx *ctx, float *mass, const int32_t *page_tabl
     a.keep_last = keep_last;
     void *const caches[4] = {k_cache, v_cache, index_cache, kv4_cache};
     const int bytes[4] = {2 * d, 2 * d, 2 * sd::kIndexDim, sd::kv4_record_bytes(d)};
-    for (int k = 0; k < 4; ++k) {
-      a.cache[k] = static_cast<uint8_t *>(caches[k]);
-      a.row_bytes[k] = bytes[k];
-    }
+    for (int k = 0; k < 4; ++k)
+      if (caches[k]) {
+        a.cache[a.n_caches] = static_cast<uint8_t *>(caches[k]);
+        a.row_bytes[a.n_caches++] = bytes[k];
+      }
     a.err = ctx->err_d;
     const cudaError_t e = sd::launch_evict(a, ctx->sh, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SD_OK : cuda_fail(ctx, e, "evict launch");

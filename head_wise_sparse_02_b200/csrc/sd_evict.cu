@@ -12,9 +12,15 @@
 //         summed through distributed shared memory, finds the key tau of the
 //         last weight kept and how many of its ties are.  Positions above tau,
 //         the first ties and the forced ones leave in ascending order.
-//   move  rows are copied 16 bytes per lane; the old pages are only read, so
-//         any number of CTAs can work on one sequence.
-// Bound: bytes, 4 N per (b, g) read once for the search, and each kept row read
+//         Bound by instructions: a thread takes four positions at a time (one
+//         page lookup and one 16-byte load; a page's weights of a head are 64
+//         bytes), and the zeros, the weights of rows that nothing attended to
+//         and usually the most common value, are counted in a register instead
+//         of one histogram bin that all lanes would queue at.
+//   move  rows are copied 16 bytes per lane, several loads in flight per thread;
+//         the old pages are only read, so any number of CTAs can work on one
+//         sequence.
+// Floor: bytes, 4 N per (b, g) read once for the search, and each kept row read
 // and written once.
 #include <algorithm>
 #include <map>
@@ -36,8 +42,11 @@ constexpr int kMaxCluster = 8;          // portable cluster size
 constexpr int kMinSlice = 2048;         // positions per CTA below which a cluster has no more CTAs
 constexpr int kBins = 2048;             // 11 bits a pass
 constexpr size_t kKeepKeysMax = 128 * 1024;   // bytes of keys held in shared memory, at most
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+constexpr uint32_t kZeroKey = 0x80000000u;    // order_key(0)
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 32;           // rows per move CTA
+constexpr int kMoveBatch = 4;           // loads in flight per thread
+constexpr int kMoveMany = 1 << 16;      // rows from which a move CTA takes 128 instead of 32
 
 __device__ __forceinline__ long long clamped_len(const EvictArgs &a, const Shape &sh, int b) {
   const long long N = a.seq_lens[b];
@@ -49,6 +58,7 @@ struct KeepShared {
   uint32_t sum[kBins];
   uint32_t wgt[kKeepWarps], weq[kKeepWarps];         // per warp: kept outright, ties of tau
   uint32_t gt, eq;                                   // the same of the CTA (read by the cluster)
+  uint32_t share;                                    // counts in this CTA's share of the bins
   uint32_t digit, above;
   uint32_t wsum[kKeepWarps];
 };
@@ -57,7 +67,7 @@ struct KeepShared {
 template <bool KEYS>
 __global__ void __launch_bounds__(kKeepThreads)
 evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ KeepShared S;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
@@ -75,17 +85,21 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
   const int mid0 = a.keep_first, mid1 = N - a.keep_last;         // positions the weights decide about
   const bool all = N <= a.budget;
   const int32_t *pt = a.page_table + (long long)b * sh.max_pages;
-  auto key_of = [&](int j) -> uint32_t {
-    const int page = pt[j / kPage];
-    if (page < 0 || page >= sh.num_pages) return 0u;             // reported by the move
-    return order_key(__ldcg(a.mass + ((long long)page * sh.Hkv + g) * kPage + j % kPage));
+  // keys of the positions j .. j + 3 (j a multiple of four: one page)
+  auto load4 = [&](int j) -> uint4 {
+    const int page = __ldg(pt + j / kPage);
+    if (page < 0 || page >= sh.num_pages) return make_uint4(0u, 0u, 0u, 0u);   // reported by the move
+    const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.mass + ((long long)page * sh.Hkv + g) * kPage + j % kPage));
+    return make_uint4(order_key(v.x), order_key(v.y), order_key(v.z), order_key(v.w));
   };
+  uint4 *keys4 = reinterpret_cast<uint4 *>(keys);
+  auto keys_at = [&](int j) -> uint4 { return KEYS ? keys4[(j - j0) / 4] : load4(j); };
   uint32_t tau = 0u;
   int need = 0;                                                  // ties of tau that stay
   if (!all) {
     if (KEYS) {
 #pragma unroll 4
-      for (int j = j0 + tid; j < j1; j += kKeepThreads) keys[j - j0] = key_of(j);
+      for (int j = j0 + 4 * tid; j < j1; j += 4 * kKeepThreads) keys4[(j - j0) / 4] = load4(j);
       __syncthreads();
     }
     need = a.budget - a.keep_first - a.keep_last;
@@ -98,22 +112,57 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
       for (int x = tid; x < bins; x += kKeepThreads) S.hist[x] = 0u;
       __syncthreads();
       const int lo = std::max(j0, mid0), hi = std::min(j1, mid1);
-      for (int j = lo + tid; j < hi; j += kKeepThreads) {
-        const uint32_t k = KEYS ? keys[j - j0] : key_of(j);
-        if ((k & mask) == prefix) atomicAdd(&S.hist[(k >> shift) & (bins - 1)], 1u);
+      uint32_t zeros = 0u;
+      for (int j = lo / 4 * 4 + 4 * tid; j < hi; j += 4 * kKeepThreads) {
+        const uint4 k4 = keys_at(j);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        const bool inner = j >= lo && j + 4 <= hi;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (!inner && (j + u < lo || j + u >= hi)) continue;
+          if (k[u] == kZeroKey) ++zeros;
+          else if ((k[u] & mask) == prefix) atomicAdd(&S.hist[(k[u] >> shift) & (bins - 1)], 1u);
+        }
       }
+      zeros = __reduce_add_sync(kFull, zeros);
+      if (lane == 0 && zeros && (kZeroKey & mask) == prefix) atomicAdd(&S.hist[(kZeroKey >> shift) & (bins - 1)], zeros);
       cl.sync();
-      // counts of the whole cluster, from the highest bin down
-      uint32_t mine[kBins / kKeepThreads], tot = 0u;
-      const int per = bins / kKeepThreads;                       // 4 or 2 bins a thread
+      // bins of the whole cluster: CTA r sums share r of them (counted from the
+      // highest bin), so that each histogram is read once over the cluster
+      const int share = bins / C;
+      uint32_t tot = 0u;
+      for (int x = tid; x < share; x += kKeepThreads) {
+        const int bin = bins - 1 - (rank * share + x);
+        uint32_t n = 0u;
+        for (int r = 0; r < C; ++r) n += cl.map_shared_rank(S.hist, r)[bin];
+        S.sum[x] = n;
+        tot += n;
+      }
+      tot = __reduce_add_sync(kFull, tot);
+      if (lane == 0) S.wsum[warp] = tot;
+      __syncthreads();
+      if (tid == 0) {
+        uint32_t n = 0u;
+        for (int w = 0; w < kKeepWarps; ++w) n += S.wsum[w];
+        S.share = n;
+      }
+      cl.sync();                                                 // every histogram read, every share summed
+      // the share that holds the need-th count from the top, then its bin
+      uint32_t before = 0u;
+      int owner = 0;
+      for (; owner < C - 1; ++owner) {
+        const uint32_t n = *cl.map_shared_rank(&S.share, owner);
+        if (before + n >= (uint32_t)need) break;
+        before += n;
+      }
+      const uint32_t *sum = cl.map_shared_rank(S.sum, owner);
+      uint32_t mine[kBins / kKeepThreads];
+      tot = 0u;
 #pragma unroll
       for (int u = 0; u < kBins / kKeepThreads; ++u) {
-        mine[u] = 0u;
-        if (u < per) {
-          const int x = bins - 1 - (tid * per + u);
-          for (int r = 0; r < C; ++r) mine[u] += cl.map_shared_rank(S.hist, r)[x];
-          tot += mine[u];
-        }
+        const int x = tid * (kBins / kKeepThreads) + u;
+        mine[u] = x < share ? sum[x] : 0u;
+        tot += mine[u];
       }
       uint32_t incl = tot;
 #pragma unroll
@@ -121,20 +170,20 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
         const uint32_t y = __shfl_up_sync(kFull, incl, o);
         if (lane >= o) incl += y;
       }
+      __syncthreads();                                           // wsum read
       if (lane == 31) S.wsum[warp] = incl;
       __syncthreads();
-      uint32_t run = incl - tot;
+      uint32_t run = before + incl - tot;
       for (int w = 0; w < warp; ++w) run += S.wsum[w];
 #pragma unroll
-      for (int u = 0; u < kBins / kKeepThreads; ++u)
-        if (u < per) {
-          if (run < (uint32_t)need && run + mine[u] >= (uint32_t)need) {   // exactly one thread
-            S.digit = (uint32_t)(bins - 1 - (tid * per + u));
-            S.above = run;
-          }
-          run += mine[u];
+      for (int u = 0; u < kBins / kKeepThreads; ++u) {
+        if (run < (uint32_t)need && run + mine[u] >= (uint32_t)need) {     // exactly one thread
+          S.digit = (uint32_t)(bins - 1 - (owner * share + tid * (kBins / kKeepThreads) + u));
+          S.above = run;
         }
-      cl.sync();                                                 // digit set; every histogram read
+        run += mine[u];
+      }
+      __syncthreads();
       prefix |= S.digit << shift;
       mask |= (uint32_t)(bins - 1) << shift;
       need -= (int)S.above;
@@ -142,23 +191,35 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
     tau = prefix;
   }
   const bool some = !all && a.budget - a.keep_first - a.keep_last > 0;
-  // 0 evicted, 1 kept, 2 a tie of tau
-  auto state = [&](int j) -> int {
-    if (j >= j1) return 0;
-    if (all || j < mid0 || j >= mid1) return 1;
-    if (!some) return 0;
-    const uint32_t k = KEYS ? keys[j - j0] : key_of(j);
-    return k > tau ? 1 : (k == tau ? 2 : 0);
+  // of the positions j .. j + 3: how many stay outright (low half) and are ties
+  // of tau (high half), and which (bits 0-3 and 4-7 of `bits`)
+  auto count4 = [&](int j, uint32_t &bits) -> uint32_t {
+    bits = 0u;
+    if (j >= j1) return 0u;
+    uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
+    if (some) k4 = keys_at(j);
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool forced = all || j + u < mid0 || j + u >= mid1;
+      const bool one = forced || (some && k[u] > tau);
+      if (j + u < j1) bits |= one ? 1u << u : ((some && k[u] == tau) ? 16u << u : 0u);
+    }
+    return __popc(bits & 0xFu) | ((uint32_t)__popc(bits & 0xF0u) << 16);
   };
-  // warp w owns a run of the slice: its counts, then the places of its positions
-  const int run = ((j1 - j0 + kKeepWarps - 1) / kKeepWarps + 31) / 32 * 32;
+  // warp w owns a run of the slice (whole steps of 128 positions): its counts,
+  // then the places of its positions
+  const int run = ((j1 - j0 + kKeepWarps - 1) / kKeepWarps + 127) / 128 * 128;
   const int w0 = std::min(j1, j0 + warp * run), w1 = std::min(j1, w0 + run);
   uint32_t n1 = 0u, n2 = 0u;
-  for (int j = w0; j < w1; j += 32) {
-    const int s = j + lane < w1 ? state(j + lane) : 0;
-    n1 += __popc(__ballot_sync(kFull, s == 1));
-    n2 += __popc(__ballot_sync(kFull, s == 2));
+  for (int j = w0; j < w1; j += 128) {
+    uint32_t bits;
+    const uint32_t n = count4(j + 4 * lane, bits);
+    n1 += n & 0xFFFFu;
+    n2 += n >> 16;
   }
+  n1 = __reduce_add_sync(kFull, n1);
+  n2 = __reduce_add_sync(kFull, n2);
   if (lane == 0) {
     S.wgt[warp] = n1;
     S.weq[warp] = n2;
@@ -184,39 +245,44 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
     eq += S.weq[w];
   }
   int32_t *kept = a.kept + ((long long)b * sh.Hkv + g) * a.budget;
-  for (int j = w0; j < w1; j += 32) {
-    const int s = j + lane < w1 ? state(j + lane) : 0;
-    const unsigned b1 = __ballot_sync(kFull, s == 1), b2 = __ballot_sync(kFull, s == 2);
-    const unsigned below = (1u << lane) - 1u;
-    const uint32_t g1 = gt + __popc(b1 & below), e1 = eq + __popc(b2 & below);
-    if (s == 1 || (s == 2 && e1 < (uint32_t)need)) kept[g1 + std::min(e1, (uint32_t)need)] = j + lane;
-    gt += __popc(b1);
-    eq += __popc(b2);
+  for (int j = w0; j < w1; j += 128) {
+    uint32_t bits;
+    const uint32_t n = count4(j + 4 * lane, bits);
+    uint32_t incl = n;                                             // both counts at once: at most 128 each
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += y;
+    }
+    uint32_t g1 = gt + ((incl - n) & 0xFFFFu), e1 = eq + ((incl - n) >> 16);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool one = bits & (1u << u), tie = bits & (16u << u);
+      if (one || (tie && e1 < (uint32_t)need)) kept[g1 + std::min(e1, (uint32_t)need)] = j + 4 * lane + u;
+      g1 += one;
+      e1 += tie;
+    }
+    const uint32_t tot = __shfl_sync(kFull, incl, 31);
+    gt += tot & 0xFFFFu;
+    eq += tot >> 16;
   }
   cl.sync();                                                     // no CTA leaves while its counts are read
 }
 
-// Copies the rows of one cache, CH chunks of 16 bytes each
-template <int CH>
-__device__ __forceinline__ void move_rows(uint8_t *cache, const uint32_t *src, const uint32_t *dst, int n) {
-  uint4 *base = reinterpret_cast<uint4 *>(cache);
-#pragma unroll 4
-  for (int x = threadIdx.x; x < n * CH; x += kMoveThreads) {
-    const int i = x / CH, c = x % CH;
-    if (src[i] != 0xFFFFFFFFu) base[(size_t)dst[i] * CH + c] = __ldcg(base + (size_t)src[i] * CH + c);
-  }
-}
-
+// ROWS rows per CTA.  The rows of all caches form one index space of 16-byte
+// chunks, row by row, cache by cache within a row; chunk x of the CTA's rows is
+// chunk x % total of row x / total (by a multiplication: x < 2^13, total <= 64).
+template <int ROWS>
 __global__ void __launch_bounds__(kMoveThreads)
-evict_move_kernel(const EvictArgs a, const Shape sh) {
-  __shared__ uint32_t src[kMoveRows], dst[kMoveRows];
+evict_move_kernel(const EvictArgs a, const Shape sh, int total, uint32_t inverse) {
+  __shared__ uint32_t src[ROWS], dst[ROWS];
   const int tid = threadIdx.x;
   const int item = blockIdx.x, b = item / sh.Hkv, g = item % sh.Hkv;
   pdl_wait();
   pdl_trigger();
   const int keep = std::min((int)clamped_len(a, sh, b), a.budget);
-  const int i0 = blockIdx.y * kMoveRows;
-  const int n = keep - i0 < kMoveRows ? keep - i0 : kMoveRows;
+  const int i0 = blockIdx.y * ROWS;
+  const int n = keep - i0 < ROWS ? keep - i0 : ROWS;
   if (n <= 0) return;
   if (tid < n) {
     const int j = __ldcg(a.kept + ((long long)b * sh.Hkv + g) * a.budget + i0 + tid);
@@ -226,22 +292,47 @@ evict_move_kernel(const EvictArgs a, const Shape sh) {
     const int to = a.new_page_table[(long long)b * sh.max_pages + i / kPage];
     const bool ok = from >= 0 && from < sh.num_pages && to >= 0 && to < sh.num_pages;
     if (!ok) raise_error(a.err, in ? SD_EBIT_PAGE : SD_EBIT_SEL);
-    src[tid] = ok ? (uint32_t)(((long long)from * sh.Hkv + g) * kPage + j % kPage) : 0xFFFFFFFFu;
-    dst[tid] = ok ? (uint32_t)(((long long)to * sh.Hkv + g) * kPage + i % kPage) : 0u;
+    src[tid] = ok ? ((uint32_t)from * sh.Hkv + g) * kPage + j % kPage : kNoRow;
+    dst[tid] = ok ? ((uint32_t)to * sh.Hkv + g) * kPage + i % kPage : 0u;
     if (ok) a.mass[dst[tid]] = __ldcg(a.mass + src[tid]);
   }
   __syncthreads();
+  for (int x0 = tid; x0 < n * total; x0 += kMoveBatch * kMoveThreads) {
+    uint4 v[kMoveBatch];
+    uint4 *to[kMoveBatch];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (!a.cache[k]) continue;
-    switch (a.row_bytes[k]) {
-      case 32: move_rows<2>(a.cache[k], src, dst, n); break;
-      case 80: move_rows<5>(a.cache[k], src, dst, n); break;
-      case 128: move_rows<8>(a.cache[k], src, dst, n); break;
-      case 160: move_rows<10>(a.cache[k], src, dst, n); break;
-      default: move_rows<16>(a.cache[k], src, dst, n); break;
+    for (int u = 0; u < kMoveBatch; ++u) {
+      const int x = x0 + u * kMoveThreads;
+      to[u] = nullptr;
+      if (x >= n * total) continue;
+      const int i = (int)(((uint32_t)x * inverse) >> 19);
+      int c = x - i * total;
+      uint8_t *base = a.cache[0];
+      int bytes = a.row_bytes[0];
+#pragma unroll
+      for (int k = 1; k < 4; ++k)
+        if (c * 16 >= bytes && k < a.n_caches) {     // not in the caches before
+          c -= bytes / 16;
+          base = a.cache[k];
+          bytes = a.row_bytes[k];
+        }
+      if (src[i] == kNoRow) continue;
+      v[u] = __ldcg(reinterpret_cast<const uint4 *>(base + (size_t)src[i] * bytes) + c);
+      to[u] = reinterpret_cast<uint4 *>(base + (size_t)dst[i] * bytes) + c;
     }
+#pragma unroll
+    for (int u = 0; u < kMoveBatch; ++u)
+      if (to[u]) *to[u] = v[u];
   }
+}
+
+template <int ROWS>
+cudaError_t launch_move(const EvictArgs &a, const Shape &sh, cudaStream_t st) {
+  int total = 0;
+  for (int k = 0; k < a.n_caches; ++k) total += a.row_bytes[k] / 16;
+  const uint32_t inverse = total > 0 ? (1u << 19) / total + 1 : 0u;
+  return launch_pdl(evict_move_kernel<ROWS>, dim3((unsigned)(a.batch * sh.Hkv), (unsigned)((a.budget + ROWS - 1) / ROWS)),
+                    dim3(kMoveThreads), 0, st, 0, a, sh, total, inverse);
 }
 
 template <bool KEYS>
@@ -274,8 +365,8 @@ cudaError_t launch_evict(const EvictArgs &a, const Shape &sh, cudaStream_t st) {
   const cudaError_t e = bytes <= kKeepKeysMax ? launch_keep<true>(a, sh, C, slice_pages, bytes, st)
                                               : launch_keep<false>(a, sh, C, slice_pages, 0, st);
   if (e != cudaSuccess) return e;
-  return launch_pdl(evict_move_kernel, dim3((unsigned)(a.batch * sh.Hkv), (unsigned)((a.budget + kMoveRows - 1) / kMoveRows)),
-                    dim3(kMoveThreads), 0, st, 0, a, sh);
+  // few rows: small CTAs, so that every SM has some
+  return (long long)a.batch * sh.Hkv * a.budget >= kMoveMany ? launch_move<128>(a, sh, st) : launch_move<32>(a, sh, st);
 }
 
 }  // namespace sd

@@ -329,9 +329,10 @@ struct EvictArgs {
   int32_t *new_lens;              // [B]
   int batch;
   int budget, keep_first, keep_last;
-  // caches whose rows move (null = absent): base and bytes of one row
+  // caches whose rows move: base and bytes of one row (a multiple of 16)
   uint8_t *cache[4];
   int row_bytes[4];
+  int n_caches;
   unsigned *err;
 };
 cudaError_t launch_evict(const EvictArgs &a, const Shape &sh, cudaStream_t st);

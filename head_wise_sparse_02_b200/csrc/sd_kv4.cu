@@ -9,11 +9,12 @@
 // so a channel of the group is off by at most s / 2 (plus what the rounding of
 // s moves the top of the range: less than 15 * 2^-9 s).
 //
-// Both kernels are bound by bytes (append 4 d read and 5 d / 4 written per
-// token and KV head, load the reverse).  A quad of lanes takes a group, eight
-// channels (one 16-byte load) per lane, so the group's range is two exchanges
-// away and a lane's codes are exactly one 32-bit word of the record; d / 8
-// lanes take a row, and a row's codes leave in one coalesced store.
+// Floor of both: bytes (append 4 d read and 5 d / 4 written per token and KV
+// head, load the reverse).  A quad of lanes takes a group, eight channels (one
+// 16-byte load) per lane, so the group's range is two exchanges away and a
+// lane's codes are exactly one 32-bit word of the record; d / 8 lanes take a
+// row, and a row's codes leave in one coalesced store.  With many tokens a warp
+// takes four (token, head) pairs at a time, whose loads are in flight together.
 #include "sd_internal.cuh"
 
 namespace sd {
@@ -28,142 +29,208 @@ struct Place {
   static constexpr int NG = D / kKv4Group;
   static constexpr int kLanes = D / 8;               // lanes per row
   static constexpr int kUnits = 32 / (2 * kLanes);   // (token, head) pairs per warp
-  long long unit;
-  int part, g, t;
-  __device__ explicit Place(int lane, long long warp)
-      : unit(warp * kUnits + lane / (2 * kLanes)), part(lane / kLanes % 2), g(lane % kLanes / 4), t(lane % 4) {}
+  int part, g, t, tok, head;                         // tok past the end: nothing to do
+  // U steps per warp: steps of one warp are kUnits pairs apart
+  __device__ Place(int lane, uint32_t warp, int U, const Shape &sh)
+      : part(lane / kLanes % 2), g(lane % kLanes / 4), t(lane % 4) {
+    const uint32_t unit = warp * U * kUnits + lane / (2 * kLanes);
+    tok = (int)(unit / (uint32_t)sh.Hkv);
+    head = (int)(unit - (uint32_t)tok * sh.Hkv);
+  }
+  __device__ void next(const Shape &sh) {
+    head += kUnits;
+    while (head >= sh.Hkv) {
+      head -= sh.Hkv;
+      ++tok;
+    }
+  }
 };
 
 // slot -> record, or -1 (with the error bit) when the slot is outside the pool
 __device__ __forceinline__ long long record_of(int slot, int head, const Shape &sh, unsigned *err, bool report) {
-  if (slot < 0 || slot >= (long long)sh.num_pages * kPage) {
+  if (slot < 0 || slot / kPage >= sh.num_pages) {
     if (report) raise_error(err, SD_EBIT_SLOT);
     return -1;
   }
-  return ((long long)(slot / kPage) * sh.Hkv + head) * kPage + slot % kPage;
+  return ((uint32_t)(slot / kPage) * sh.Hkv + head) * kPage + slot % kPage;   // below 2^32 by init's check
 }
 
-template <int D>
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {   // NaN if either is
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The eight codes of a lane's channels w (bf16 pairs), in order from the low
+// nibble.  float32 quotients are within 3 * 2^-24 * 15.1 < 3e-6 of the true ones
+// unless s is close to the subnormal numbers; a lane with one of those, or with a
+// quotient within 1e-5 of a rounding border, decides in float64.
+__device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[4], float lo, float s) {
+  if (!(s > 0.0f)) return 0u;
+  const float inv = __frcp_rn(s);
+  constexpr float kRint = 12582912.0f;               // 1.5 * 2^23: adding and taking it off rounds to nearest even
+  float off = 0.0f, part[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float acc = 8388608.0f;                          // 2^23 + the four codes as one 16-bit number, exact
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = w[2 * h + i / 2];
+      const float t = ((i & 1 ? bf16_hi(u) : bf16_lo(u)) - lo) * inv;
+      const float q = (t + kRint) - kRint;
+      off = fmaxf(off, fabsf(t - q));
+      acc = fmaf(q, (float)(1 << (4 * i)), acc);
+    }
+    part[h] = acc;
+  }
+  if (off > 0.49999f || s < 1e-30f) {
+    uint32_t codes = 0;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t u = i < 2 ? w[0] : i < 4 ? w[1] : i < 6 ? w[2] : w[3];
+      const double x = i & 1 ? bf16_hi(u) : bf16_lo(u);
+      codes |= (uint32_t)fmin(rint((x - (double)lo) / (double)s), 15.0) << (4 * i);
+    }
+    return codes;
+  }
+  return __byte_perm(__float_as_uint(part[0]), __float_as_uint(part[1]), 0x5410);
+}
+
+template <int D, int U>
 __global__ void __launch_bounds__(kThreads)
 kv4_append_kernel(const uint16_t *__restrict__ k_new, const uint16_t *__restrict__ v_new,
                   const int32_t *__restrict__ slots, int T, uint8_t *__restrict__ kv4, const Shape sh, unsigned *err) {
   using P = Place<D>;
   constexpr int NG = P::NG;
   const int lane = threadIdx.x & 31;
-  const P at(lane, ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5);
+  P at(lane, blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), U, sh);
   pdl_wait();
   pdl_trigger();
-  const long long units = (long long)T * sh.Hkv;
-  const bool live = at.unit < units;                 // lanes past the end stay for the exchanges
-  const int tok = live ? (int)(at.unit / sh.Hkv) : 0, head = live ? (int)(at.unit % sh.Hkv) : 0;
-  uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-  if (live)
-    raw = __ldg(reinterpret_cast<const uint4 *>((at.part ? v_new : k_new) + ((long long)tok * sh.Hkv + head) * D) +
-                at.g * 4 + at.t);
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  float x[8];
-  bool finite = true;
+  uint4 raw[U];
+  int slot[U], head[U];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo(w[i]);
-    x[2 * i + 1] = bf16_hi(w[i]);
-    finite &= (w[i] & 0x7F80u) != 0x7F80u && (w[i] & 0x7F800000u) != 0x7F800000u;
-  }
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-  }
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
-  }
-  const float range = hi - lo;
-  finite &= range <= 3.402823466e38f;                // false for an overflow and for NaN
-  const unsigned bad = __ballot_sync(kFull, !finite);
-  const bool broken = (bad >> (lane & ~3)) & 0xFu;   // somewhere in the quad's group
-  if (broken) lo = 0.0f;
-  // s rounded to bf16 (nearest even); a non-finite group stands for zeros
-  const float sf = broken ? 0.0f : __fdiv_rn(range, 15.0f);
-  const uint32_t sb = (__float_as_uint(sf) + 0x7FFFu + ((__float_as_uint(sf) >> 16) & 1u)) >> 16;
-  const float s = __uint_as_float(sb << 16);
-  uint32_t codes = 0;
-  if (s > 0.0f) {
-    // float32 quotients are within 3 * 2^-24 * 15.1 of the true ones unless s is
-    // close to the subnormal numbers; those and the ones next to a rounding
-    // border are decided in float64
-    const bool tiny = s < 1e-30f;
-    const float inv = __fdiv_rn(1.0f, s);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float t = (x[i] - lo) * inv;
-      float q = rintf(t);
-      if (tiny || fabsf(t - q) > 0.499f) q = (float)rint(((double)x[i] - (double)lo) / (double)s);
-      codes |= (uint32_t)fminf(q, 15.0f) << (4 * i);
+  for (int k = 0; k < U; ++k) {
+    raw[k] = make_uint4(0u, 0u, 0u, 0u);
+    slot[k] = head[k] = -1;                          // lanes past the end stay for the exchanges
+    if (at.tok < T) {
+      head[k] = at.head;
+      slot[k] = __ldg(slots + at.tok);
+      raw[k] = __ldg(reinterpret_cast<const uint4 *>((at.part ? v_new : k_new) + ((size_t)at.tok * sh.Hkv + at.head) * D) +
+                     at.g * 4 + at.t);
     }
+    at.next(sh);
   }
-  // value codes: the 16-bit word of channels 4 c .. 4 c + 3 of a group sits next to the next group's
-  const uint32_t other = __shfl_xor_sync(kFull, codes, 4);
-  const uint32_t lob = __float_as_uint(lo) >> 16;
-  const uint32_t sb2 = __shfl_xor_sync(kFull, sb, 4), lob2 = __shfl_xor_sync(kFull, lob, 4);
-  if (!live) return;
-  const long long rec = record_of(slots[tok], head, sh, err, lane % (2 * P::kLanes) == 0 && head == 0);
-  if (rec < 0) return;
-  if (broken && at.t == 0) raise_error(err, SD_EBIT_VALUE);
-  uint32_t *out = reinterpret_cast<uint32_t *>(kv4 + rec * kv4_record_bytes(D));
-  const bool odd = at.g & 1;
-  if (at.part == 0)
-    out[at.t * NG + at.g] = codes;
-  else if (!odd)
-    out[D / 8 + (2 * at.t * NG + at.g) / 2] = (codes & 0xFFFFu) | (other << 16);
-  else
-    out[D / 8 + ((2 * at.t + 1) * NG + at.g) / 2] = (other >> 16) | (codes & 0xFFFF0000u);
-  uint32_t *meta = out + D / 4 + at.part * NG + at.g / 2;
-  if (!odd && at.t == 0) meta[0] = sb | (sb2 << 16);
-  if (!odd && at.t == 1) meta[NG / 2] = lob | (lob2 << 16);
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+    // (min x, min -x) of the group
+    const uint32_t lo2 = min_bf16x2(min_bf16x2(w[0], w[1]), min_bf16x2(w[2], w[3]));
+    constexpr uint32_t kNeg = 0x80008000u;
+    const uint32_t nh2 = min_bf16x2(min_bf16x2(w[0] ^ kNeg, w[1] ^ kNeg), min_bf16x2(w[2] ^ kNeg, w[3] ^ kNeg));
+    uint32_t mm = min_bf16x2(__byte_perm(lo2, nh2, 0x5410), __byte_perm(lo2, nh2, 0x7632));
+    mm = min_bf16x2(mm, __shfl_xor_sync(kFull, mm, 1));
+    mm = min_bf16x2(mm, __shfl_xor_sync(kFull, mm, 2));
+    float lo = bf16_lo(mm);
+    const float range = -bf16_hi(mm) - lo;
+    const bool broken = !(range <= 3.402823466e38f); // NaN, an infinity or an overflow: stands for zeros
+    if (broken) lo = 0.0f;
+    // s rounded to bf16, nearest even
+    const uint32_t sf = broken ? 0u : __float_as_uint(__fdiv_rn(range, 15.0f));
+    const uint32_t sb = (sf + 0x7FFFu + ((sf >> 16) & 1u)) >> 16;
+    const uint32_t codes = codes_of(w, lo, __uint_as_float(sb << 16));
+    // value codes: the 16-bit word of channels 4 c .. 4 c + 3 of a group sits next to the next group's
+    const uint32_t other = __shfl_xor_sync(kFull, codes, 4);
+    const uint32_t lob = __float_as_uint(lo) >> 16;
+    const uint32_t pair = __shfl_xor_sync(kFull, sb | (lob << 16), 4);
+    if (head[k] < 0) continue;
+    const long long rec = record_of(slot[k], head[k], sh, err, lane % (2 * P::kLanes) == 0 && head[k] == 0);
+    if (rec < 0) continue;
+    if (broken && at.t == 0) raise_error(err, SD_EBIT_VALUE);
+    uint32_t *out = reinterpret_cast<uint32_t *>(kv4 + rec * kv4_record_bytes(D));
+    const bool odd = at.g & 1;
+    // one store per lane: key words as they are, value half-words two groups at a time
+    const int at_word = at.part == 0 ? at.t * NG + at.g : D / 8 + ((2 * at.t + odd) * NG + at.g - odd) / 2;
+    out[at_word] = at.part == 0 ? codes : odd ? __byte_perm(other, codes, 0x7632) : __byte_perm(codes, other, 0x5410);
+    uint32_t *meta = out + D / 4 + at.part * NG + at.g / 2;
+    if (!odd && at.t < 2) meta[at.t * (NG / 2)] = at.t ? __byte_perm(lob, pair, 0x7610) : __byte_perm(sb, pair, 0x5410);
+  }
 }
 
-template <int D>
+template <int D, int U>
 __global__ void __launch_bounds__(kThreads)
 kv4_load_kernel(const uint8_t *__restrict__ kv4, const int32_t *__restrict__ slots, int T,
                 uint16_t *__restrict__ k_out, uint16_t *__restrict__ v_out, const Shape sh, unsigned *err) {
   using P = Place<D>;
   constexpr int NG = P::NG;
   const int lane = threadIdx.x & 31;
-  const P at(lane, ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5);
+  P at(lane, blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), U, sh);
   pdl_wait();
   pdl_trigger();
-  if (at.unit >= (long long)T * sh.Hkv) return;
-  const int tok = (int)(at.unit / sh.Hkv), head = (int)(at.unit % sh.Hkv);
-  const long long rec = record_of(slots[tok], head, sh, err, lane % (2 * P::kLanes) == 0 && head == 0);
-  if (rec < 0) return;
-  const uint8_t *in = kv4 + rec * kv4_record_bytes(D);
-  uint32_t codes;
-  if (at.part == 0) {
-    codes = reinterpret_cast<const uint32_t *>(in)[at.t * NG + at.g];
-  } else {
-    const uint16_t *v = reinterpret_cast<const uint16_t *>(in + D / 2);
-    codes = v[2 * at.t * NG + at.g] | ((uint32_t)v[(2 * at.t + 1) * NG + at.g] << 16);
-  }
-  const uint16_t *meta = reinterpret_cast<const uint16_t *>(in + D) + at.part * 2 * NG;
-  const float s = bf16_to_f32(meta[at.g]), lo = bf16_to_f32(meta[NG + at.g]);
-  uint32_t o[4];
+  long long rec[U];
+  uint32_t unit[U];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = fmaf(s, (float)((codes >> (8 * i)) & 15u), lo);
-    const float b = fmaf(s, (float)((codes >> (8 * i + 4)) & 15u), lo);
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(o[i]) : "f"(b), "f"(a));
+  for (int k = 0; k < U; ++k) {
+    rec[k] = -1;
+    unit[k] = (uint32_t)at.tok * sh.Hkv + at.head;
+    if (at.tok < T)
+      rec[k] = record_of(__ldg(slots + at.tok), at.head, sh, err, lane % (2 * P::kLanes) == 0 && at.head == 0);
+    at.next(sh);
   }
-  reinterpret_cast<uint4 *>((at.part ? v_out : k_out) + ((long long)tok * sh.Hkv + head) * D)[at.g * 4 + at.t] =
-      make_uint4(o[0], o[1], o[2], o[3]);
+  uint32_t codes[U], s2[U], lo2[U];
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    codes[k] = s2[k] = lo2[k] = 0u;
+    if (rec[k] < 0) continue;
+    const uint8_t *in = kv4 + rec[k] * kv4_record_bytes(D);
+    if (at.part == 0) {
+      codes[k] = reinterpret_cast<const uint32_t *>(in)[at.t * NG + at.g];
+    } else {
+      const uint16_t *v = reinterpret_cast<const uint16_t *>(in + D / 2);
+      codes[k] = v[2 * at.t * NG + at.g] | ((uint32_t)v[(2 * at.t + 1) * NG + at.g] << 16);
+    }
+    const uint16_t *meta = reinterpret_cast<const uint16_t *>(in + D) + at.part * 2 * NG;
+    s2[k] = meta[at.g] * 0x10001u;
+    lo2[k] = meta[NG + at.g] * 0x10001u;
+  }
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    if (rec[k] < 0) continue;
+    // channels i and i + 4 of the eight: 128 + code is exact in bf16, and the
+    // fused multiply-add rounds lo + s code once
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("{.reg .b32 c; sub.rn.bf16x2 c, %1, %2; fma.rn.bf16x2 %0, c, %3, %4;}\n"
+          : "=r"(o[i])
+          : "r"(((codes[k] >> (4 * i)) & 0x000F000Fu) | 0x43004300u), "r"(0x43004300u), "r"(s2[k]), "r"(lo2[k]));
+    reinterpret_cast<uint4 *>((at.part ? v_out : k_out) + (size_t)unit[k] * D)[at.g * 4 + at.t] =
+        make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410), __byte_perm(o[0], o[1], 0x7632),
+                   __byte_perm(o[2], o[3], 0x7632));
+  }
 }
 
-template <int D>
+// (token, head) pairs per warp step and how many steps at once: four when that
+// still leaves every SM warps to hide the loads behind
+constexpr int kManyUnits = 32768;
+
+template <int D, int U>
 dim3 grid_of(int T, const Shape &sh) {
-  const long long per = (long long)(kThreads / 32) * Place<D>::kUnits;
+  const long long per = (long long)(kThreads / 32) * Place<D>::kUnits * U;
   return dim3((unsigned)(((long long)T * sh.Hkv + per - 1) / per));
+}
+
+template <int D, int U>
+cudaError_t append_t(const uint16_t *k_new, const uint16_t *v_new, const int32_t *slots, int T, uint8_t *kv4,
+                     const Shape &sh, unsigned *err, cudaStream_t st) {
+  return launch_pdl(kv4_append_kernel<D, U>, grid_of<D, U>(T, sh), dim3(kThreads), 0, st, 0, k_new, v_new, slots, T, kv4,
+                    sh, err);
+}
+
+template <int D, int U>
+cudaError_t load_t(const uint8_t *kv4, const int32_t *slots, int T, uint16_t *k_out, uint16_t *v_out, const Shape &sh,
+                   unsigned *err, cudaStream_t st) {
+  return launch_pdl(kv4_load_kernel<D, U>, grid_of<D, U>(T, sh), dim3(kThreads), 0, st, 0, kv4, slots, T, k_out, v_out,
+                    sh, err);
 }
 
 }  // namespace
@@ -171,21 +238,23 @@ dim3 grid_of(int T, const Shape &sh) {
 cudaError_t launch_kv4_append(const uint16_t *k_new, const uint16_t *v_new, const int32_t *slots, int T, uint8_t *kv4,
                               const Shape &sh, unsigned *err, cudaStream_t st) {
   if (T == 0) return cudaSuccess;
+  const bool many = (long long)T * sh.Hkv >= kManyUnits;
   if (sh.d == 128)
-    return launch_pdl(kv4_append_kernel<128>, grid_of<128>(T, sh), dim3(kThreads), 0, st, 0, k_new, v_new, slots, T,
-                      kv4, sh, err);
-  return launch_pdl(kv4_append_kernel<64>, grid_of<64>(T, sh), dim3(kThreads), 0, st, 0, k_new, v_new, slots, T, kv4,
-                    sh, err);
+    return many ? append_t<128, 4>(k_new, v_new, slots, T, kv4, sh, err, st)
+                : append_t<128, 1>(k_new, v_new, slots, T, kv4, sh, err, st);
+  return many ? append_t<64, 4>(k_new, v_new, slots, T, kv4, sh, err, st)
+              : append_t<64, 1>(k_new, v_new, slots, T, kv4, sh, err, st);
 }
 
 cudaError_t launch_kv4_load(const uint8_t *kv4, const int32_t *slots, int T, uint16_t *k_out, uint16_t *v_out,
                             const Shape &sh, unsigned *err, cudaStream_t st) {
   if (T == 0) return cudaSuccess;
+  const bool many = (long long)T * sh.Hkv >= kManyUnits;
   if (sh.d == 128)
-    return launch_pdl(kv4_load_kernel<128>, grid_of<128>(T, sh), dim3(kThreads), 0, st, 0, kv4, slots, T, k_out, v_out,
-                      sh, err);
-  return launch_pdl(kv4_load_kernel<64>, grid_of<64>(T, sh), dim3(kThreads), 0, st, 0, kv4, slots, T, k_out, v_out, sh,
-                    err);
+    return many ? load_t<128, 4>(kv4, slots, T, k_out, v_out, sh, err, st)
+                : load_t<128, 1>(kv4, slots, T, k_out, v_out, sh, err, st);
+  return many ? load_t<64, 4>(kv4, slots, T, k_out, v_out, sh, err, st)
+              : load_t<64, 1>(kv4, slots, T, k_out, v_out, sh, err, st);
 }
 
 }  // namespace sd

@@ -496,7 +496,9 @@ SD_API sd_status sparse_decode_attend_noalloc(sd_ctx *ctx, const void *q, const 
  * A slot outside the pool sets SD_EBIT_SLOT and is skipped.  A group with a NaN
  * or an infinity, or whose range exceeds float32, sets SD_EBIT_VALUE and is
  * stored as zeros, so records are always finite.  The same slot twice in a call
- * leaves an unspecified mix of the two tokens.  num_tokens == 0 is a no-op.
+ * leaves an unspecified mix of the two tokens.  num_tokens == 0 is a no-op;
+ * num_tokens * Hkv must stay below 2^31 (SD_ERR_UNSUPPORTED), here and in
+ * sparse_decode_kv4_load.
  */
 SD_API sd_status sparse_decode_kv4_append(sd_ctx *ctx, const void *k_new, const void *v_new, const int32_t *slots,
                                    int num_tokens, void *kv4_cache, sd_stream stream);
@@ -504,7 +506,7 @@ SD_API sd_status sparse_decode_kv4_append(sd_ctx *ctx, const void *k_new, const 
 /*
  * sparse_decode_kv4_load -- read `num_tokens` tokens back as bf16:
  *
- *   k_out[t, g, :] = bf16_rne( float32( lo + s * code ) )  of slot slots[t]
+ *   k_out[t, g, :] = bf16_rne( lo + s * code )  of slot slots[t]
  *
  * (and likewise v), for the calls that take bf16 caches (prefill of a later
  * chunk, exact-score selection).
@@ -555,7 +557,7 @@ SD_API sd_status sparse_decode_select_attend_kv4(sd_ctx *ctx, const void *q_pre,
  * in every run, unless sequences of the batch share pages: their weights then
  * all count, added in no fixed order.
  *
- *   mass       device float32 [num_pages, Hkv, P], updated in place.
+ *   mass       device float32 [num_pages, Hkv, P], 16-byte aligned, updated in place.
  *   workspace  at least sparse_decode_mass_workspace_size bytes.
  */
 SD_API sd_status sparse_decode_attend_mass(sd_ctx *ctx, const void *q, const void *k_cache, const void *v_cache,
@@ -599,7 +601,7 @@ SD_API sd_status sparse_decode_mass_workspace_size(const sd_ctx *ctx, int batch,
  * other sequences stay valid for those.  With keep_first >= num_sinks and
  * keep_last >= window the local heads' sets are unchanged.
  *
- *   mass            device float32 [num_pages, Hkv, P].  A NaN counts above
+ *   mass            device float32 [num_pages, Hkv, P], 16-byte aligned.  A NaN counts above
  *                   every number if its sign bit is clear, below if set.
  *   new_page_table  device int32 [B, MAXP]; entries [0, ceil(n_b / P)) name
  *                   pages that no sequence of the batch uses, each once (rows of
