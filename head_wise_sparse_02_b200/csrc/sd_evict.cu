@@ -16,7 +16,9 @@
 //         page lookup and one 16-byte load; a page's weights of a head are 64
 //         bytes), and the zeros, the weights of rows that nothing attended to
 //         and usually the most common value, are counted in a register instead
-//         of one histogram bin that all lanes would queue at.
+//         of one histogram bin that all lanes would queue at.  The kept weights
+//         themselves are written to the new pages from here: gathered later, 4
+//         bytes would cost 64 of DRAM traffic each.
 //   move  rows are copied 16 bytes per lane, several loads in flight per thread;
 //         the old pages are only read, so any number of CTAs can work on one
 //         sequence.
@@ -38,7 +40,7 @@ namespace cg = cooperative_groups;
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kKeepThreads = 512;
 constexpr int kKeepWarps = kKeepThreads / 32;
-constexpr int kMaxCluster = 8;          // portable cluster size
+constexpr int kMaxCluster = 8;          // CTAs per cluster, at most
 constexpr int kMinSlice = 2048;         // positions per CTA below which a cluster has no more CTAs
 constexpr int kBins = 2048;             // 11 bits a pass
 constexpr size_t kKeepKeysMax = 128 * 1024;   // bytes of keys held in shared memory, at most
@@ -97,11 +99,6 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
   uint32_t tau = 0u;
   int need = 0;                                                  // ties of tau that stay
   if (!all) {
-    if (KEYS) {
-#pragma unroll 4
-      for (int j = j0 + 4 * tid; j < j1; j += 4 * kKeepThreads) keys4[(j - j0) / 4] = load4(j);
-      __syncthreads();
-    }
     need = a.budget - a.keep_first - a.keep_last;
     const int widths[3] = {11, 11, 10};
     uint32_t prefix = 0u, mask = 0u;
@@ -111,10 +108,18 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
       shift -= bits;
       for (int x = tid; x < bins; x += kKeepThreads) S.hist[x] = 0u;
       __syncthreads();
-      const int lo = std::max(j0, mid0), hi = std::min(j1, mid1);
+      const int lo = std::max(j0, mid0), hi = std::min(j1, mid1);  // of the positions the weights decide about
       uint32_t zeros = 0u;
-      for (int j = lo / 4 * 4 + 4 * tid; j < hi; j += 4 * kKeepThreads) {
-        const uint4 k4 = keys_at(j);
+      // the first pass loads the slice (each thread comes back to its own positions)
+#pragma unroll 4
+      for (int j = j0 + 4 * tid; j < j1; j += 4 * kKeepThreads) {
+        uint4 k4;
+        if (pass == 0) {
+          k4 = load4(j);
+          if (KEYS) keys4[(j - j0) / 4] = k4;
+        } else {
+          k4 = keys_at(j);
+        }
         const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
         const bool inner = j >= lo && j + 4 <= hi;
 #pragma unroll
@@ -190,13 +195,13 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
     }
     tau = prefix;
   }
+  __syncthreads();                                               // every thread's keys
   const bool some = !all && a.budget - a.keep_first - a.keep_last > 0;
   // of the positions j .. j + 3: how many stay outright (low half) and are ties
   // of tau (high half), and which (bits 0-3 and 4-7 of `bits`)
-  auto count4 = [&](int j, uint32_t &bits) -> uint32_t {
+  auto count4 = [&](int j, uint32_t &bits, uint4 &k4) -> uint32_t {
     bits = 0u;
     if (j >= j1) return 0u;
-    uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
     if (some) k4 = keys_at(j);
     const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
@@ -214,7 +219,8 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
   uint32_t n1 = 0u, n2 = 0u;
   for (int j = w0; j < w1; j += 128) {
     uint32_t bits;
-    const uint32_t n = count4(j + 4 * lane, bits);
+    uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t n = count4(j + 4 * lane, bits, k4);
     n1 += n & 0xFFFFu;
     n2 += n >> 16;
   }
@@ -244,10 +250,15 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
     gt += S.wgt[w];
     eq += S.weq[w];
   }
+  cg::cluster_group::arrival_token token = cl.barrier_arrive();  // this CTA has read the others' counts
   int32_t *kept = a.kept + ((long long)b * sh.Hkv + g) * a.budget;
+  const int32_t *npt = a.new_page_table + (long long)b * sh.max_pages;
   for (int j = w0; j < w1; j += 128) {
     uint32_t bits;
-    const uint32_t n = count4(j + 4 * lane, bits);
+    uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t n = count4(j + 4 * lane, bits, k4);
+    if (!some && bits) k4 = load4(j + 4 * lane);                   // the weights move with their rows
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
     uint32_t incl = n;                                             // both counts at once: at most 128 each
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -258,7 +269,13 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const bool one = bits & (1u << u), tie = bits & (16u << u);
-      if (one || (tie && e1 < (uint32_t)need)) kept[g1 + std::min(e1, (uint32_t)need)] = j + 4 * lane + u;
+      if (one || (tie && e1 < (uint32_t)need)) {
+        const int i = (int)(g1 + std::min(e1, (uint32_t)need));
+        kept[i] = j + 4 * lane + u;
+        const int page = __ldg(npt + i / kPage);
+        if (k[u] != 0u && page >= 0 && page < sh.num_pages)       // bad pages are reported by the move
+          a.mass[((long long)page * sh.Hkv + g) * kPage + i % kPage] = key_to_float(k[u]);
+      }
       g1 += one;
       e1 += tie;
     }
@@ -266,7 +283,7 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
     gt += tot & 0xFFFFu;
     eq += tot >> 16;
   }
-  cl.sync();                                                     // no CTA leaves while its counts are read
+  cl.barrier_wait(std::move(token));                             // no CTA leaves while its counts are read
 }
 
 // ROWS rows per CTA.  The rows of all caches form one index space of 16-byte
@@ -294,7 +311,6 @@ evict_move_kernel(const EvictArgs a, const Shape sh, int total, uint32_t inverse
     if (!ok) raise_error(a.err, in ? SD_EBIT_PAGE : SD_EBIT_SEL);
     src[tid] = ok ? ((uint32_t)from * sh.Hkv + g) * kPage + j % kPage : kNoRow;
     dst[tid] = ok ? ((uint32_t)to * sh.Hkv + g) * kPage + i % kPage : 0u;
-    if (ok) a.mass[dst[tid]] = __ldcg(a.mass + src[tid]);
   }
   __syncthreads();
   for (int x0 = tid; x0 < n * total; x0 += kMoveBatch * kMoveThreads) {
@@ -338,16 +354,18 @@ cudaError_t launch_move(const EvictArgs &a, const Shape &sh, cudaStream_t st) {
 template <bool KEYS>
 cudaError_t launch_keep(const EvictArgs &a, const Shape &sh, int C, int slice_pages, size_t bytes, cudaStream_t st) {
   static std::mutex mu;
-  static std::map<int, size_t> done;                             // per device
-  if (bytes > 0) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
+  static std::map<int, bool> done;                               // per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
     std::lock_guard<std::mutex> lk(mu);
-    if (done[dev] < kKeepKeysMax) {
+    if (!done[dev]) {
       e = cudaFuncSetAttribute(evict_keep_kernel<KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kKeepKeysMax);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(evict_keep_kernel<KEYS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
-      done[dev] = kKeepKeysMax;
+      done[dev] = true;
     }
   }
   return launch_pdl(evict_keep_kernel<KEYS>, dim3((unsigned)(a.batch * sh.Hkv * C)), dim3(kKeepThreads), bytes, st, C, a,

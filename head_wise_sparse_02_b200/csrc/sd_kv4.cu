@@ -61,39 +61,61 @@ __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {   // Na
   return r;
 }
 
+// The code of a quotient on or next to the border between two codes, q one of
+// them: by the exact d - q s when d = x - lo is exact, else in float64.
+__device__ __noinline__ float code_f64(float x, float lo, float s) {
+  return (float)fmin(rint(((double)x - (double)lo) / (double)s), 15.0);
+}
+__device__ __forceinline__ float border_code(float x, float lo, float s, float d, float e, float q, bool tiny) {
+  const float back = d - x, err = (x - (d - back)) - (lo + back);   // x - lo = d + err
+  if (err != 0.0f || tiny) return code_f64(x, lo, s);
+  const float half = 0.5f * s;
+  const bool odd = (int)q & 1;
+  if (e > half || (e == half && odd)) return q + 1.0f;
+  if (e < -half || (e == -half && odd)) return q - 1.0f;
+  return q;
+}
 // The eight codes of a lane's channels w (bf16 pairs), in order from the low
-// nibble.  float32 quotients are within 3 * 2^-24 * 15.1 < 3e-6 of the true ones
-// unless s is close to the subnormal numbers; a lane with one of those, or with a
-// quotient within 1e-5 of a rounding border, decides in float64.
+// nibble.  A float32 quotient gives a candidate, and d - q s (one fused
+// operation, exact) tells whether it is the nearest: only lanes with a quotient
+// on or next to the border between two codes look again.  Ties are common, since
+// d and s have few bits.
 __device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[4], float lo, float s) {
   if (!(s > 0.0f)) return 0u;
-  const float inv = __frcp_rn(s);
+  float inv;
+  asm("rcp.approx.f32 %0, %1;\n" : "=f"(inv) : "f"(s));
   constexpr float kRint = 12582912.0f;               // 1.5 * 2^23: adding and taking it off rounds to nearest even
-  float off = 0.0f, part[2];
+  const float half = 0.5f * s;
+  float off = 0.0f, q[8];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float acc = 8388608.0f;                          // 2^23 + the four codes as one 16-bit number, exact
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t u = w[2 * h + i / 2];
-      const float t = ((i & 1 ? bf16_hi(u) : bf16_lo(u)) - lo) * inv;
-      const float q = (t + kRint) - kRint;
-      off = fmaxf(off, fabsf(t - q));
-      acc = fmaf(q, (float)(1 << (4 * i)), acc);
-    }
-    part[h] = acc;
+  for (int i = 0; i < 8; ++i) {
+    const float d = (i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2])) - lo;
+    q[i] = fmaf(d, inv, kRint) - kRint;
+    off = fmaxf(off, fabsf(fmaf(-q[i], s, d)));
   }
-  if (off > 0.49999f || s < 1e-30f) {
-    uint32_t codes = 0;
-#pragma unroll 1
+  const bool tiny = s < 1e-30f;
+  if (off > 0.9999f * half || tiny) {
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t u = i < 2 ? w[0] : i < 4 ? w[1] : i < 6 ? w[2] : w[3];
-      const double x = i & 1 ? bf16_hi(u) : bf16_lo(u);
-      codes |= (uint32_t)fmin(rint((x - (double)lo) / (double)s), 15.0) << (4 * i);
+      const float x = i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+      const float d = x - lo, e = fmaf(-q[i], s, d);
+      if (tiny || fabsf(e) > 0.9999f * half) q[i] = border_code(x, lo, s, d, e, q[i], tiny);
     }
-    return codes;
   }
+  float part[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)                        // 2^23 + the four codes as one 16-bit number, exact
+    part[h] = fmaf(q[4 * h + 3], 4096.0f, fmaf(q[4 * h + 2], 256.0f, fmaf(q[4 * h + 1], 16.0f, q[4 * h] + 8388608.0f)));
   return __byte_perm(__float_as_uint(part[0]), __float_as_uint(part[1]), 0x5410);
+}
+
+// x / 15 rounded to nearest (Markstein: one correction of the product with the
+// rounded reciprocal is enough while nothing is subnormal)
+__device__ __forceinline__ float fifteenth(float x) {
+  if (x < 1e-30f) return __fdiv_rn(x, 15.0f);
+  constexpr float r = 1.0f / 15.0f;
+  const float q = x * r;
+  return fmaf(fmaf(-15.0f, q, x), r, q);
 }
 
 template <int D, int U>
@@ -135,7 +157,7 @@ kv4_append_kernel(const uint16_t *__restrict__ k_new, const uint16_t *__restrict
     const bool broken = !(range <= 3.402823466e38f); // NaN, an infinity or an overflow: stands for zeros
     if (broken) lo = 0.0f;
     // s rounded to bf16, nearest even
-    const uint32_t sf = broken ? 0u : __float_as_uint(__fdiv_rn(range, 15.0f));
+    const uint32_t sf = broken ? 0u : __float_as_uint(fifteenth(range));
     const uint32_t sb = (sf + 0x7FFFu + ((sf >> 16) & 1u)) >> 16;
     const uint32_t codes = codes_of(w, lo, __uint_as_float(sb << 16));
     // value codes: the 16-bit word of channels 4 c .. 4 c + 3 of a group sits next to the next group's
@@ -182,12 +204,9 @@ kv4_load_kernel(const uint8_t *__restrict__ kv4, const int32_t *__restrict__ slo
     codes[k] = s2[k] = lo2[k] = 0u;
     if (rec[k] < 0) continue;
     const uint8_t *in = kv4 + rec[k] * kv4_record_bytes(D);
-    if (at.part == 0) {
-      codes[k] = reinterpret_cast<const uint32_t *>(in)[at.t * NG + at.g];
-    } else {
-      const uint16_t *v = reinterpret_cast<const uint16_t *>(in + D / 2);
-      codes[k] = v[2 * at.t * NG + at.g] | ((uint32_t)v[(2 * at.t + 1) * NG + at.g] << 16);
-    }
+    // the halves of a key word are neighbours, those of a value word NG apart
+    const uint16_t *c = reinterpret_cast<const uint16_t *>(in) + (at.part ? D / 4 + 2 * at.t * NG + at.g : 2 * (at.t * NG + at.g));
+    codes[k] = c[0] | ((uint32_t)c[at.part ? NG : 1] << 16);
     const uint16_t *meta = reinterpret_cast<const uint16_t *>(in + D) + at.part * 2 * NG;
     s2[k] = meta[at.g] * 0x10001u;
     lo2[k] = meta[NG + at.g] * 0x10001u;
