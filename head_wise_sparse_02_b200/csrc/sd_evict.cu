@@ -57,7 +57,6 @@ __device__ __forceinline__ long long clamped_len(const EvictArgs &a, const Shape
 
 struct KeepShared {
   uint32_t hist[kBins];
-  uint32_t sum[kBins];
   uint32_t wgt[kKeepWarps], weq[kKeepWarps];         // per warp: kept outright, ties of tau
   uint32_t gt, eq;                                   // the same of the CTA (read by the cluster)
   uint32_t share;                                    // counts in this CTA's share of the bins
@@ -65,14 +64,15 @@ struct KeepShared {
   uint32_t wsum[kKeepWarps];
 };
 
-// dynamic shared memory: the slice's keys (when they fit)
+// dynamic shared memory: [cluster sums of this CTA's share of the bins: kBins / C][the slice's keys, when they fit]
 template <bool KEYS>
 __global__ void __launch_bounds__(kKeepThreads)
 evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
-  extern __shared__ __align__(16) uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t dyn[];
   __shared__ KeepShared S;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  uint32_t *sums = dyn;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int item = blockIdx.x / C, b = item / sh.Hkv, g = item % sh.Hkv;
   pdl_wait();
@@ -94,7 +94,7 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
     const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.mass + ((long long)page * sh.Hkv + g) * kPage + j % kPage));
     return make_uint4(order_key(v.x), order_key(v.y), order_key(v.z), order_key(v.w));
   };
-  uint4 *keys4 = reinterpret_cast<uint4 *>(keys);
+  uint4 *keys4 = reinterpret_cast<uint4 *>(dyn + kBins / C);
   auto keys_at = [&](int j) -> uint4 { return KEYS ? keys4[(j - j0) / 4] : load4(j); };
   uint32_t tau = 0u;
   int need = 0;                                                  // ties of tau that stay
@@ -140,7 +140,7 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
         const int bin = bins - 1 - (rank * share + x);
         uint32_t n = 0u;
         for (int r = 0; r < C; ++r) n += cl.map_shared_rank(S.hist, r)[bin];
-        S.sum[x] = n;
+        sums[x] = n;
         tot += n;
       }
       tot = __reduce_add_sync(kFull, tot);
@@ -160,7 +160,7 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
         if (before + n >= (uint32_t)need) break;
         before += n;
       }
-      const uint32_t *sum = cl.map_shared_rank(S.sum, owner);
+      const uint32_t *sum = cl.map_shared_rank(sums, owner);
       uint32_t mine[kBins / kKeepThreads];
       tot = 0u;
 #pragma unroll
@@ -266,18 +266,20 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
       if (lane >= o) incl += y;
     }
     uint32_t g1 = gt + ((incl - n) & 0xFFFFu), e1 = eq + ((incl - n) >> 16);
+    int at[4], page[4];                                            // slot of each kept position, its page
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const bool one = bits & (1u << u), tie = bits & (16u << u);
-      if (one || (tie && e1 < (uint32_t)need)) {
-        const int i = (int)(g1 + std::min(e1, (uint32_t)need));
-        kept[i] = j + 4 * lane + u;
-        const int page = __ldg(npt + i / kPage);
-        if (k[u] != 0u && page >= 0 && page < sh.num_pages)       // bad pages are reported by the move
-          a.mass[((long long)page * sh.Hkv + g) * kPage + i % kPage] = key_to_float(k[u]);
-      }
+      at[u] = one || (tie && e1 < (uint32_t)need) ? (int)(g1 + std::min(e1, (uint32_t)need)) : -1;
+      page[u] = at[u] >= 0 ? __ldg(npt + at[u] / kPage) : -1;
       g1 += one;
       e1 += tie;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (at[u] >= 0) kept[at[u]] = j + 4 * lane + u;
+      if (k[u] != 0u && page[u] >= 0 && page[u] < sh.num_pages)    // bad pages are reported by the move
+        a.mass[((long long)page[u] * sh.Hkv + g) * kPage + at[u] % kPage] = key_to_float(k[u]);
     }
     const uint32_t tot = __shfl_sync(kFull, incl, 31);
     gt += tot & 0xFFFFu;
@@ -347,6 +349,21 @@ cudaError_t launch_move(const EvictArgs &a, const Shape &sh, cudaStream_t st) {
   int total = 0;
   for (int k = 0; k < a.n_caches; ++k) total += a.row_bytes[k] / 16;
   const uint32_t inverse = total > 0 ? (1u << 19) / total + 1 : 0u;
+  static std::mutex mu;
+  static std::map<int, bool> done;                               // per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (!done[dev]) {
+      // the loads in flight want L1, not what the search left as shared memory
+      e = cudaFuncSetAttribute(evict_move_kernel<ROWS>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxL1);
+      if (e != cudaSuccess) return e;
+      done[dev] = true;
+    }
+  }
   return launch_pdl(evict_move_kernel<ROWS>, dim3((unsigned)(a.batch * sh.Hkv), (unsigned)((a.budget + ROWS - 1) / ROWS)),
                     dim3(kMoveThreads), 0, st, 0, a, sh, total, inverse);
 }
@@ -361,9 +378,8 @@ cudaError_t launch_keep(const EvictArgs &a, const Shape &sh, int C, int slice_pa
   {
     std::lock_guard<std::mutex> lk(mu);
     if (!done[dev]) {
-      e = cudaFuncSetAttribute(evict_keep_kernel<KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kKeepKeysMax);
-      if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(evict_keep_kernel<KEYS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      e = cudaFuncSetAttribute(evict_keep_kernel<KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)(kKeepKeysMax + kBins * sizeof(uint32_t)));
       if (e != cudaSuccess) return e;
       done[dev] = true;
     }
@@ -379,9 +395,9 @@ cudaError_t launch_evict(const EvictArgs &a, const Shape &sh, cudaStream_t st) {
   int C = 1;
   while (C < kMaxCluster && (long long)C * kMinSlice < sh.max_len) C *= 2;
   const int slice_pages = (sh.max_pages + C - 1) / C;
-  const size_t bytes = (size_t)slice_pages * kPage * sizeof(uint32_t);
-  const cudaError_t e = bytes <= kKeepKeysMax ? launch_keep<true>(a, sh, C, slice_pages, bytes, st)
-                                              : launch_keep<false>(a, sh, C, slice_pages, 0, st);
+  const size_t keys = (size_t)slice_pages * kPage * sizeof(uint32_t), sums = kBins / C * sizeof(uint32_t);
+  const cudaError_t e = keys <= kKeepKeysMax ? launch_keep<true>(a, sh, C, slice_pages, sums + keys, st)
+                                             : launch_keep<false>(a, sh, C, slice_pages, sums, st);
   if (e != cudaSuccess) return e;
   // few rows: small CTAs, so that every SM has some
   return (long long)a.batch * sh.Hkv * a.budget >= kMoveMany ? launch_move<128>(a, sh, st) : launch_move<32>(a, sh, st);
