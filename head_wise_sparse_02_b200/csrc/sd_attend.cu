@@ -119,14 +119,83 @@ __device__ void item_prefix(const AttendArgs &a, const Shape &sh, const Tables &
   if (tid == 0) ws.tstart[ap.ni] = carry;
 }
 
+// Shares for a main kernel whose CTAs take one item each, by the layout's CTA
+// after item_prefix: item i of t_i tiles gets ceil(t_i / per) CTAs, each an equal
+// part of it, with `per` just large enough that all fit the grid.  `grid` CTAs
+// are resident at once; many items take several times that, so that an item of
+// average size still has more than one CTA.
+constexpr int kMinSegTiles = 8;         // tiles a CTA takes at least (two per warp) before an item gets another
+constexpr int kLayoutItems = 2048;      // items whose first CTAs are searched in shared memory
+
+__device__ void item_segments(const AttParams &ap, const AttWs &ws, int grid) {
+  __shared__ int cs[kLayoutItems + 1];
+  __shared__ int wsum[32];
+  __shared__ int carry;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  __syncthreads();
+  const long long W = ws.tstart[ap.ni];
+  const int waves = (2 * ap.ni + grid - 1) / grid;
+  const long long room = std::max<long long>(std::min<long long>((long long)grid * std::max(1, waves), kMaxSegments) - ap.ni, 1);
+  const long long per = std::max<long long>(kMinSegTiles, (W + room - 1) / room);
+  const bool small = ap.ni <= kLayoutItems;
+  if (tid == 0) carry = 0;
+  __syncthreads();
+  for (int base = 0; base < ap.ni; base += blockDim.x) {
+    const int i = base + tid;
+    const int n = i < ap.ni ? (int)((ws.tstart[i + 1] - ws.tstart[i] + per - 1) / per) : 0;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    int before = carry, total = 0;
+    for (int w = 0; w < nw; ++w) {
+      if (w < warp) before += wsum[w];
+      total += wsum[w];
+    }
+    if (i < ap.ni) {
+      if (small) cs[i] = before + incl - n;
+      else ws.cstart[i] = before + incl - n;
+    }
+    __syncthreads();
+    if (tid == 0) carry += total;
+    __syncthreads();
+  }
+  const int ns = carry;
+  if (tid == 0) {
+    ws.n_seg[0] = ns;
+    if (small) cs[ap.ni] = ns;
+    else ws.cstart[ap.ni] = ns;
+  }
+  __syncthreads();
+  const int *first = small ? cs : ws.cstart;
+  for (int c = tid; c < ns; c += blockDim.x) {
+    int lo = 0, hi = ap.ni;                            // last item with first[lo] <= c
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first[mid] <= c) lo = mid;
+      else hi = mid;
+    }
+    const int c0 = first[lo], n = first[lo + 1] - c0;
+    const long long t0 = ws.tstart[lo], t = ws.tstart[lo + 1] - t0;
+    const int a0 = (int)(t * (c - c0) / n), a1 = (int)(t * (c - c0 + 1) / n);
+    ws.seg[c] = Segment{lo, a0, a1 - a0, c0, c0 + n - 1, ws.item_rows[lo], t0 + a0};
+  }
+}
+
 // The item layout, one CTA, after the plan (when there is one) has summed the
-// retrieval items' rows.
+// retrieval items' rows; seg_grid > 0: the CTAs' shares as well.
 template <int D>
 __global__ void __launch_bounds__(1024)
-attend_prefix_kernel(const AttendArgs a, const Shape sh, const Tables tb, const AttParams ap, const AttWs ws) {
+attend_prefix_kernel(const AttendArgs a, const Shape sh, const Tables tb, const AttParams ap, const AttWs ws,
+                     int seg_grid) {
   pdl_wait();
   pdl_trigger();
   item_prefix<D>(a, sh, tb, ap, ws);
+  if (seg_grid > 0) item_segments(ap, ws, seg_grid);
 }
 
 // ============================================================== plan kernel
@@ -326,7 +395,7 @@ attend_plan_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
 // MASS: every logit, with its tile's cache rows, is left in the workspace for
 // the weights pass (sd_mass.cu)
 template <int D, int GR, bool MASS>
-__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, D == 128 ? 2 : GR > 8 ? 3 : 4)
 attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const AttParams ap, const AttWs ws) {
   constexpr int KS = D / 16;                         // k-steps of Q K^T
   constexpr int NT = D / 8;                          // n-tiles (8 dims) of P V
@@ -682,7 +751,7 @@ attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
         cacc[(warp * GR + gq + 8) * D + cc + 1] = o[nn][3];
       }
     }
-    merge_segment<D, GR, MASS>(a, sh, ws, S, dyn, GR, c, item, first, last, b, nh);
+    merge_segment<D, GR, MASS, kWarps>(a, sh, ws, S, dyn, GR, c + item, item, first, last, first + item, b, nh);
     t = seg_end;
     if (tid == 0) S.item = item + 1;
   }
@@ -714,7 +783,7 @@ AttParams att_params(const Shape &sh, const Tables &tb, int batch) {
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct AttLayout {
-  size_t partials, plan_row, plan_mask, plan_cnt, tstart, counters, total;
+  size_t partials, plan_row, plan_mask, plan_cnt, tstart, counters, seg, total;
   size_t logits, tile_row, tile_item, lse, total_mass;                // accumulated weights: behind the rest
 };
 
@@ -730,6 +799,7 @@ AttLayout att_layout(const Shape &sh, const Tables &tb, int batch, long long loc
   L.plan_cnt = o;  o = align256(o + (size_t)batch * tb.n_ret * p.ns * 4);
   L.tstart = o;    o = align256(o + (size_t)(p.ni + 1) * 8);
   L.counters = o;  o = align256(o + (size_t)p.ni * 2 * 4);           // item_rows, tickets
+  L.seg = o;       o = align256(o + (size_t)std::max(kMaxSegments, p.ni + 1) * sizeof(Segment) + (size_t)(p.ni + 2) * 4);
   L.total = o;
   const size_t loc_tiles = (size_t)((std::min(sh.max_len, local_rows) + kTileRows - 1) / kTileRows);
   const size_t tiles = (size_t)batch * ((size_t)tb.n_ret * sh.max_pages + (size_t)tb.n_loc * loc_tiles);
@@ -769,7 +839,9 @@ cudaError_t launch_t(const AttendArgs &a, const Shape &sh, const Tables &tb, con
     e = launch_pdl(attend_plan_kernel<D, GR>, grid, dim3(kPlanThreads), pbytes, st, 0, a, sh, tb, p, ws, only);
     if (e != cudaSuccess) return e;
   }
-  e = launch_pdl(attend_prefix_kernel<D>, dim3(1), dim3(1024), 0, st, 0, a, sh, tb, p, ws);
+  const int seg_grid = a.kv4 ? kv4_main_grid(sh, tb, p, GR, a.mass != nullptr) : 0;
+  if (a.kv4 && seg_grid <= 0) return cudaErrorInvalidConfiguration;
+  e = launch_pdl(attend_prefix_kernel<D>, dim3(1), dim3(1024), 0, st, 0, a, sh, tb, p, ws, seg_grid);
   if (e != cudaSuccess) return e;
   if (a.kv4)
     e = launch_attend_kv4_main(a, sh, tb, p, ws, GR, st);
@@ -823,6 +895,9 @@ cudaError_t launch_attend(const AttendArgs &a, const Shape &sh, const Tables &tb
   ws.tstart = reinterpret_cast<long long *>(base + L.tstart);
   ws.item_rows = reinterpret_cast<int *>(base + L.counters);
   ws.tickets = reinterpret_cast<unsigned *>(ws.item_rows + p.ni);
+  ws.seg = reinterpret_cast<Segment *>(base + L.seg);
+  ws.cstart = reinterpret_cast<int *>(ws.seg + std::max(kMaxSegments, p.ni + 1));
+  ws.n_seg = ws.cstart + p.ni + 1;
   if (a.mass) {
     ws.logits = reinterpret_cast<float *>(base + L.logits);
     ws.tile_row = reinterpret_cast<uint32_t *>(base + L.tile_row);

@@ -18,6 +18,16 @@ struct AttParams {
   int ni;                   // all items: then B * n_loc local items
 };
 
+// A CTA's share of one item, for a main kernel whose CTAs take one item each
+// (written by the layout): 32 bytes.
+struct Segment {
+  int item;
+  int tile0, tiles;         // of the item's tiles
+  int first, last;          // CTAs that hold the item
+  int rows;                 // of the item
+  long long tile;           // tile0 among all tiles
+};
+
 // Carving of the attend workspace.
 struct AttWs {
   float *partials;          // [(kMaxGrid + ni) slots][GR][D + 2]
@@ -27,6 +37,10 @@ struct AttWs {
   long long *tstart;        // [ni + 1]: first tile of each item; tstart[ni] = all tiles
   int *item_rows;           // [ni]: rows of each item (layout)
   unsigned *tickets;        // [ni]: partials merged per item (cleared by the layout)
+  // for a main kernel whose CTAs take one item each
+  Segment *seg;             // [max(kMaxSegments, ni + 1)]
+  int *cstart;              // [ni + 1]: first CTA of each item
+  int *n_seg;               // their number
   // accumulated weights only (null otherwise)
   float *logits;            // [tiles][heads per item][16]: base-2 logits, -inf where masked
   uint32_t *tile_row;       // [tiles][16]: cache row of each logit column, kNoRow where there is none
@@ -44,6 +58,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTileRows = 16;
 constexpr int kMaxGrid = 4096;          // persistent CTAs (partial slots are sized for this)
+constexpr int kMaxSegments = 2048;      // CTAs that take one item each, at most (or one per item and one more)
 constexpr uint32_t kNoRow = 0xFFFFFFFFu; // no cache row (configurations reaching this row number are refused)
 constexpr int kMergeChunk = 64;         // partial slots weighed per step of the final merge
 
@@ -164,34 +179,35 @@ struct MainShared {
 };
 
 // The end of one segment (a CTA's share of one item), by the whole CTA.  The
-// warps have left their (m, l, acc) in dyn: [kWarps][16] m, [kWarps][16] l,
-// [kWarps][GR][D] acc, m and l relative to base-2 references.  An item that
+// NW warps have left their (m, l, acc) in dyn: [NW][16] m, [NW][16] l,
+// [NW][GR][D] acc, m and l relative to base-2 references.  An item that
 // lies inside this CTA (first == last) goes to out; otherwise the CTA writes a
-// partial and the CTA that takes the item's last ticket merges the partials of
-// CTAs first .. last (no waiting).  gr: heads per partial slot.  MASS: the
+// partial to its slot and the CTA that takes the item's last ticket merges the
+// partials of CTAs first .. last, in the slots from slot0 on (no waiting).  gr: heads per partial slot.  MASS: the
 // reference and the sum of each head also go to ws.lse.
-template <int D, int GR, bool MASS>
+template <int D, int GR, bool MASS, int NW>
 __device__ __forceinline__ void merge_segment(const AttendArgs &a, const Shape &sh, const AttWs &ws, MainShared &S,
-                                              unsigned char *dyn, int gr, long long c, int item, long long first,
-                                              long long last, int b, int nh) {
+                                              unsigned char *dyn, int gr, long long slot, int item, long long first,
+                                              long long last, long long slot0, int b, int nh) {
+  constexpr int kThr = NW * 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  float *cm = reinterpret_cast<float *>(dyn);                  // [kWarps][16]
-  float *cl = cm + kWarps * 16;                                // [kWarps][16]
-  float *cacc = cl + kWarps * 16;                              // [kWarps][GR][D]
+  float *cm = reinterpret_cast<float *>(dyn);                  // [NW][16]
+  float *cl = cm + NW * 16;                                // [NW][16]
+  float *cacc = cl + NW * 16;                              // [NW][GR][D]
   __syncthreads();
   const bool alone = first == last;                  // the whole item is in this CTA
-  float *part = ws.partials + ((c + item) * gr) * (long long)(D + 2);
-  for (int x = tid; x < nh * (D + 2); x += kThreads) {
+  float *part = ws.partials + (slot * gr) * (long long)(D + 2);
+  for (int x = tid; x < nh * (D + 2); x += kThr) {
     const int i = x / (D + 2), cc = x % (D + 2);
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, cm[w * 16 + i]);
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, cm[w * 16 + i]);
     if (alone) {
       if (cc == 0 || (cc == 1 && !MASS)) continue;
       float num = 0.0f, den = 0.0f;
       if (M > -INFINITY) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < NW; ++w) {
           const float f = exp2f(cm[w * 16 + i] - M);
           den = fmaf(f, cl[w * 16 + i], den);
           if (!MASS || cc > 1) num = fmaf(f, cacc[(w * GR + i) * D + (cc - 2)], num);
@@ -211,7 +227,7 @@ __device__ __forceinline__ void merge_segment(const AttendArgs &a, const Shape &
       v = 0.0f;
       if (M > -INFINITY) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < NW; ++w) {
           const float f = exp2f(cm[w * 16 + i] - M);
           v += f * (cc == 1 ? cl[w * 16 + i] : cacc[(w * GR + i) * D + (cc - 2)]);
         }
@@ -226,19 +242,18 @@ __device__ __forceinline__ void merge_segment(const AttendArgs &a, const Shape &
     __syncthreads();
     if (S.last) {
       __threadfence();
-      // the last segment of the item: merge partial slots first + item .. last
-      // + item.  Per head i the reference M_i = max_s m_s; then, kMergeChunk
+      // the last segment of the item: merge its partial slots.  Per head i the reference M_i = max_s m_s; then, kMergeChunk
       // slots at a time, the weights f_is = 2^(m_s - M_i) (0 for an empty
       // slot) go to shared memory and every output sums f_is o_s[cc] with
       // independent loads (an item can span a few hundred CTAs)
       const int np = (int)(last - first + 1);
       const long long PS = (long long)gr * (D + 2);                // stride of the partial slots
-      constexpr int OPT = (GR * D + kThreads - 1) / kThreads;     // outputs per thread, at most
-      const float *pbase = ws.partials + (first + item) * PS;
+      constexpr int OPT = (GR * D + kThr - 1) / kThr;     // outputs per thread, at most
+      const float *pbase = ws.partials + slot0 * PS;
       float *fw = reinterpret_cast<float *>(dyn);                  // [GR][kMergeChunk]
       float *sM = fw + GR * kMergeChunk;                           // [GR]
       float *sden = sM + GR;                                       // [GR]
-      for (int i = warp; i < nh; i += kWarps) {
+      for (int i = warp; i < nh; i += NW) {
         float M = -INFINITY;
         for (int s = lane; s < np; s += 32) M = fmaxf(M, __ldcg(pbase + s * PS + i * (D + 2)));
 #pragma unroll
@@ -254,7 +269,7 @@ __device__ __forceinline__ void merge_segment(const AttendArgs &a, const Shape &
       for (int s0 = 0; s0 < np; s0 += kMergeChunk) {
         const int nc = np - s0 < kMergeChunk ? np - s0 : kMergeChunk;
         __syncthreads();                             // M ready; the previous chunk's weights consumed
-        for (int x = tid; x < nh * kMergeChunk; x += kThreads) {
+        for (int x = tid; x < nh * kMergeChunk; x += kThr) {
           const int i = x / kMergeChunk, sl = x % kMergeChunk;
           float f = 0.0f;
           if (sl < nc) {
@@ -264,7 +279,7 @@ __device__ __forceinline__ void merge_segment(const AttendArgs &a, const Shape &
           fw[i * kMergeChunk + sl] = f;
         }
         __syncthreads();
-        for (int i = warp; i < nh; i += kWarps) {
+        for (int i = warp; i < nh; i += NW) {
           float dsum = 0.0f;
           for (int sl = lane; sl < nc; sl += 32)
             dsum = fmaf(fw[i * kMergeChunk + sl], __ldcg(pbase + (s0 + sl) * PS + i * (D + 2) + 1), dsum);
@@ -272,17 +287,26 @@ __device__ __forceinline__ void merge_segment(const AttendArgs &a, const Shape &
           for (int off = 16; off > 0; off >>= 1) dsum += __shfl_xor_sync(kFull, dsum, off);
           if (lane == 0) sden[i] += dsum;
         }
+        // slots in order for every output; the loads of kBatch slots of all the
+        // thread's outputs are in flight together
+        constexpr int kBatch = OPT >= 8 ? 2 : 8;
+#pragma unroll 1
+        for (int sl = 0; sl < nc; sl += kBatch) {
+          float v[OPT][kBatch];
 #pragma unroll
-        for (int u = 0; u < OPT; ++u) {
-          const int x = tid + u * kThreads;
-          if (x < nh * D) {
-            const int i = x / D, cc = x % D;
-            const float *pp = pbase + s0 * PS + i * (D + 2) + 2 + cc;
-            const float *fi = fw + i * kMergeChunk;
-            float acc = num[u];
-#pragma unroll 8
-            for (int sl = 0; sl < nc; ++sl) acc = fmaf(fi[sl], __ldcg(pp + sl * PS), acc);
-            num[u] = acc;
+          for (int u = 0; u < OPT; ++u) {
+            const int x = tid + u * kThr;
+            const float *pp = pbase + (s0 + sl) * PS + (x / D) * (D + 2) + 2 + x % D;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) v[u][k] = x < nh * D && sl + k < nc ? __ldcg(pp + k * PS) : 0.0f;
+          }
+#pragma unroll
+          for (int u = 0; u < OPT; ++u) {
+            const int x = tid + u * kThr;
+            const float *fi = fw + (x < nh * D ? x / D : 0) * kMergeChunk + sl;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+              if (sl + k < nc) num[u] = fmaf(fi[k], v[u][k], num[u]);
           }
         }
       }
@@ -291,7 +315,7 @@ __device__ __forceinline__ void merge_segment(const AttendArgs &a, const Shape &
         ws.lse[(long long)item * kMaxGroup + tid] = make_float2(sM[tid], sden[tid] > 0.0f ? 1.0f / sden[tid] : 0.0f);
 #pragma unroll
       for (int u = 0; u < OPT; ++u) {
-        const int x = tid + u * kThreads;
+        const int x = tid + u * kThr;
         if (x < nh * D) {
           const int i = x / D, cc = x % D;
           a.out[((long long)b * sh.Hq + S.grp.q_head[i]) * D + cc] = sden[i] > 0.0f ? num[u] / sden[i] : 0.0f;
@@ -343,6 +367,8 @@ int resident_ctas(K kern, int threads, size_t smem) {
 
 // The main kernel on a 4-bit cache (sd_attend_kv4.cu), after the plan and the
 // layout; gr: heads per partial slot.
+// kv4_main_grid: CTAs of that kernel that fit the device at once (0: error).
+int kv4_main_grid(const Shape &sh, const Tables &tb, const AttParams &p, int gr, bool mass);
 cudaError_t launch_attend_kv4_main(const AttendArgs &a, const Shape &sh, const Tables &tb, const AttParams &p,
                                    const AttWs &ws, int gr, cudaStream_t st);
 // The weights pass (sd_mass.cu), after the main kernel: adds every row's

@@ -40,6 +40,8 @@
 namespace sd {
 namespace {
 
+constexpr int kWarps4 = 4;
+constexpr int kThreads4 = kWarps4 * 32;
 constexpr int kRing4 = 4;               // tiles in flight per warp
 constexpr float kLazy = 4.0f;           // a head's reference may lag its maximum by this (log2)
 constexpr int kScaleTop = 10;           // exponent of the largest p s at p = 1
@@ -113,13 +115,13 @@ __device__ __forceinline__ bool any_gt_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 __device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
 
-// dynamic shared memory: [ring: kWarps x kRing4 tiles: key codes [16][d / 2] in
+// dynamic shared memory: [ring: kWarps4 x kRing4 tiles: key codes [16][d / 2] in
 //                         column order, value codes [16][d / 2], scales [16][d / 4]]
-//                        [head masks of the tiles, in column order: kWarps x kRing4 x 16 x uint16]
+//                        [head masks of the tiles, in column order: kWarps4 x kRing4 x 16 x uint16]
 //                        [span prefix of the current item: ns + 1 ints]
 // between items the ring holds the warps' (m, l, acc) for the CTA merge
 template <int D, int GR, bool MASS>
-__global__ void __launch_bounds__(kThreads, GR > 8 ? 2 : 4)
+__global__ void __launch_bounds__(kThreads4, GR > 8 ? 2 : 4)
 attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const AttParams ap, const AttWs ws, int gr) {
   constexpr int NG = D / kKv4Group;                  // groups of channels
   constexpr int kRec = kv4_record_bytes(D);
@@ -134,21 +136,46 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
   extern __shared__ __align__(128) unsigned char dyn[];
   unsigned char *ring = dyn + warp * (kRing4 * kTileB);
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
-  uint16_t *wmask = reinterpret_cast<uint16_t *>(dyn + (size_t)kWarps * kRing4 * kTileB) + warp * (kRing4 * kTileRows);
-  int *pre = reinterpret_cast<int *>(dyn + (size_t)kWarps * kRing4 * kTileB + kWarps * kRing4 * kTileRows * 2);
+  uint16_t *wmask = reinterpret_cast<uint16_t *>(dyn + (size_t)kWarps4 * kRing4 * kTileB) + warp * (kRing4 * kTileRows);
+  int *pre = reinterpret_cast<int *>(dyn + (size_t)kWarps4 * kRing4 * kTileB + kWarps4 * kRing4 * kTileRows * 2);
   pdl_wait();
   pdl_trigger();
 
-  // ---- this CTA's share of the tiles (as in the bf16 kernel) -------------------
-  const long long W = __ldcg(ws.tstart + ap.ni);
-  const long long P = std::min<long long>(gridDim.x, W), c = blockIdx.x;
-  if (c >= P) return;
-  const long long t0 = W * c / P, t1 = W * (c + 1) / P;
-  auto cta_of = [&](long long x) { return ((x + 1) * P - 1) / W; };
-  if (warp == 0) {
-    const int i = warp_lower_bound<long long>(ws.tstart, ap.ni + 1, t0 + 1, lane) - 1;
-    if (lane == 0) S.item = i;
+  // ---- this CTA's share of one item ---------------------------------------------
+  const int n_seg = __ldcg(ws.n_seg);
+  const int4 s0 = __ldcg(reinterpret_cast<const int4 *>(ws.seg + blockIdx.x));
+  const int4 s1 = __ldcg(reinterpret_cast<const int4 *>(ws.seg + blockIdx.x) + 1);
+  if ((int)blockIdx.x >= n_seg) return;
+  const int item = s0.x, first = s0.w, last = s1.x;
+  [[maybe_unused]] const long long t = ((long long)s1.w << 32) | (uint32_t)s1.z;   // first tile among all
+  int b;
+  bool is_ret;
+  const Group &grp_g = item_group(tb, ap, item, b, is_ret);
+  const int gi = is_ret ? item % tb.n_ret : 0;
+  const long long slot0 = ((long long)b * tb.n_ret + gi) * ap.ns;
+  const int N = (int)clamp_len(a, sh, b);
+  const int ns_item = is_ret ? (N + ap.span - 1) / ap.span : 0;
+  if (tid < (int)(sizeof(Group) / 4)) reinterpret_cast<int *>(&S.grp)[tid] = reinterpret_cast<const int *>(&grp_g)[tid];
+  if (is_ret && warp == kWarps4 - 1) {
+    // exclusive prefix of the item's span counts (32 spans at a time)
+    int run = 0;
+    for (int p0 = 0; p0 < ns_item; p0 += 32) {
+      const int s = p0 + lane;
+      const int cnt = s < ns_item ? __ldcg(ws.plan_cnt + slot0 + s) : 0;
+      int incl = cnt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (s < ns_item) pre[s] = run + incl - cnt;
+      run += __shfl_sync(kFull, incl, 31);
+    }
+    if (lane == 0) pre[ns_item] = run;
   }
+  // rows of an item are below 2^25 (the longest context)
+  const int r0 = s0.y * kTileRows;
+  const int r1 = std::min(s1.y, (s0.y + s0.z) * kTileRows);
 
   // copies: lanes 2 r and 2 r + 1 take row r of a tile, the even and the odd
   // 16-byte chunks (whole sectors); where they go in the tile
@@ -165,466 +192,438 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
   const float2 lo_mul = is_lo ? make_float2(-1.0f, -1.0f) : make_float2(0.0f, 0.0f);
   const int hd = PACK ? (gq & 3) : gq;               // head (of column block 0) whose scores this lane holds
 
-  long long t = t0;
-  while (t < t1) {
-    __syncthreads();                                   // S.item set; the previous item's smem no longer read
-    int item = S.item;
-    long long ts = __ldcg(ws.tstart + item), te = __ldcg(ws.tstart + item + 1);
-    while (te <= t) {                                  // skip items without tiles
-      ++item;
-      ts = te;
-      te = __ldcg(ws.tstart + item + 1);
-    }
-    const long long seg_end = std::min(t1, te);
-    int b;
-    bool is_ret;
-    const Group &grp_g = item_group(tb, ap, item, b, is_ret);
-    if (tid == 0) S.grp = grp_g;
-    const long long N = clamp_len(a, sh, b);
-    // rows of an item are below 2^25 (the longest context): 32-bit from here on
-    const int r0 = (int)(t - ts) * kTileRows;
-    const int r1 = std::min(__ldcg(ws.item_rows + item), (int)(seg_end - ts) * kTileRows);
-    const long long first = cta_of(ts), last = cta_of(te - 1);
-    const int gi = is_ret ? item % tb.n_ret : 0;
-    const long long slot0 = ((long long)b * tb.n_ret + gi) * ap.ns;
-    const int ns_item = is_ret ? (int)((N + ap.span - 1) / ap.span) : 0;
-    if (is_ret && warp == 0) {
-      // exclusive prefix of the item's span counts (32 spans at a time)
-      int run = 0;
-      for (int s0 = 0; s0 < ns_item; s0 += 32) {
-        const int s = s0 + lane;
-        const int cnt = s < ns_item ? __ldcg(ws.plan_cnt + slot0 + s) : 0;
-        int incl = cnt;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(kFull, incl, o);
-          if (lane >= o) incl += y;
-        }
-        if (s < ns_item) pre[s] = run + incl - cnt;
-        run += __shfl_sync(kFull, incl, 31);
-      }
-      if (lane == 0) pre[ns_item] = run;
-    }
-    __syncthreads();
-    const int nh = S.grp.n;
-    const int g_kv = S.grp.kv_head;
-    const int loc_a = (int)std::min<long long>(a.num_sinks, N);
-    const int loc_w = (int)std::max<long long>(loc_a, N - a.window);
+  __syncthreads();
+  const int nh = S.grp.n;
+  const int g_kv = S.grp.kv_head;
+  const int loc_a = std::min(a.num_sinks, N);
+  const int loc_w = std::max(loc_a, N - std::min(a.window, N));
 
-    // ---- queries: A fragments (heads on M; k = the channels of the record's
-    // words: lane tq holds channels 8 tq .. 8 tq + 7 of every group, nibble pairs
-    // (i, i + 4)), and the sums over the groups' channels; all times 2^k
-    uint32_t qa[NG][2][HB][2];
-    float qs[HB][NG], qsc[HB];
+  // ---- queries: A fragments (heads on M; k = the channels of the record's
+  // words: lane tq holds channels 8 tq .. 8 tq + 7 of every group, nibble pairs
+  // (i, i + 4)), and the sums over the groups' channels; all times 2^k
+  uint32_t qa[NG][2][HB][2];
+  float qs[HB][NG], qsc[HB];
 #pragma unroll
-    for (int hb = 0; hb < HB; ++hb) {
-      const int h = hd + 8 * hb;
-      const uint16_t *qr = h < nh ? a.q + ((long long)b * sh.Hq + S.grp.q_head[h]) * D : nullptr;
-      uint4 w[NG];
-      float top = 0.0f;
+  for (int hb = 0; hb < HB; ++hb) {
+    const int h = hd + 8 * hb;
+    const uint16_t *qr = h < nh ? a.q + ((long long)b * sh.Hq + S.grp.q_head[h]) * D : nullptr;
+    uint4 w[NG];
+    float top = 0.0f;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        w[g] = make_uint4(0u, 0u, 0u, 0u);
-        if (qr) w[g] = *reinterpret_cast<const uint4 *>(qr + g * kKv4Group + 8 * tq);
-        const uint32_t u[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
+    for (int g = 0; g < NG; ++g) {
+      w[g] = make_uint4(0u, 0u, 0u, 0u);
+      if (qr) w[g] = *reinterpret_cast<const uint4 *>(qr + g * kKv4Group + 8 * tq);
+      const uint32_t u[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(u[i])), fabsf(bf16_hi(u[i]))));
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(u[i])), fabsf(bf16_hi(u[i]))));
+    }
+    top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+    const int k = std::min(90, std::max(-90, 14 - exponent_of(top)));
+    const float f = pow2i(k);
+    qsc[hb] = sc * pow2i(-k);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      // channels (0,1) (2,3) (4,5) (6,7) -> (0,4) (1,5) (2,6) (3,7)
+      qa[g][0][hb][0] = pack_f16(bf16_lo(w[g].x) * f, bf16_lo(w[g].z) * f);
+      qa[g][0][hb][1] = pack_f16(bf16_hi(w[g].x) * f, bf16_hi(w[g].z) * f);
+      qa[g][1][hb][0] = pack_f16(bf16_lo(w[g].y) * f, bf16_lo(w[g].w) * f);
+      qa[g][1][hb][1] = pack_f16(bf16_hi(w[g].y) * f, bf16_hi(w[g].w) * f);
+      float sum = ((bf16_lo(w[g].x) + bf16_hi(w[g].x)) + (bf16_lo(w[g].y) + bf16_hi(w[g].y))) +
+                  ((bf16_lo(w[g].z) + bf16_hi(w[g].z)) + (bf16_lo(w[g].w) + bf16_hi(w[g].w)));
+      sum += __shfl_xor_sync(kFull, sum, 1);
+      sum += __shfl_xor_sync(kFull, sum, 2);
+      qs[hb][g] = sum * f;
+    }
+  }
+  float m[HB], l[HB], o[HB][NG][2][4];
+  float2 olo[HB][NG];                                // two partial sums each
+  uint32_t nf[NG / 2], thr[NG / 2];                  // bf16 pairs: 2^-R_g, and the largest s it serves
+#pragma unroll
+  for (int w = 0; w < NG / 2; ++w) {
+    nf[w] = 0x3F803F80u;
+    thr[w] = 0u;
+  }
+#pragma unroll
+  for (int hb = 0; hb < HB; ++hb) {
+    m[hb] = -INFINITY;
+    l[hb] = 0.0f;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      olo[hb][g] = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) o[hb][g][mt][0] = o[hb][g][mt][1] = o[hb][g][mt][2] = o[hb][g][mt][3] = 0.0f;
+    }
+  }
+
+  // ---- stream the segment's tiles: warp w takes tiles w, w + kWarps4, ... -----
+  const int tiles = (r1 - r0 + kTileRows - 1) / kTileRows;
+  const int mt_w = tiles > warp ? (tiles - warp + kWarps4 - 1) / kWarps4 : 0;
+  const uint32_t all = (1u << nh) - 1u;
+  const uint32_t *prow = ws.plan_row + slot0 * ap.span;
+  const uint16_t *pmask = ws.plan_mask + slot0 * ap.span;
+  const int32_t *pt = a.page_table + (long long)b * sh.max_pages;
+  int sp = 0;                                        // span of the last row fetched (rows only ascend)
+  // cache row and head mask of row lane >> 1 of tile q
+  auto fetch = [&](int q, uint32_t &row, uint32_t &mask) {
+    row = 0u;
+    mask = 0u;
+    const int gx = r0 + (warp + q * kWarps4) * kTileRows + crow;
+    if (gx >= r1) return;
+    if (is_ret) {
+      while (pre[sp + 1] <= gx) ++sp;                // ends: gx < rows of the item = pre[ns_item]
+      const int e = sp * ap.span + (gx - pre[sp]);
+      row = __ldcg(prow + e);
+      mask = __ldcg(pmask + e);
+    } else {
+      const int pos = gx < loc_a ? gx : loc_w + (gx - loc_a);
+      const int page = pt[pos / kPage];
+      const bool ok = page >= 0 && page < sh.num_pages;
+      if (!ok) raise_error(a.err, SD_EBIT_PAGE);
+      row = ok ? ((uint32_t)page * sh.Hkv + g_kv) * kPage + pos % kPage : 0u;   // below 2^32 by init's check
+      mask = ok ? all : 0u;
+    }
+  };
+  // copy tile q's records; rows past the segment repeat the tile's first
+  // (finite data) and are masked out
+  auto issue = [&](int q, uint32_t row, uint32_t mask) {
+    if (q < mt_w) {
+      const int tile = warp + q * kWarps4;
+      const uint32_t row0 = __shfl_sync(kFull, row, 0);
+      if (r0 + tile * kTileRows + crow >= r1) row = row0;
+      if (!odd) {
+        wmask[(q % kRing4) * kTileRows + cplace] = (uint16_t)mask;
+        if constexpr (MASS) ws.tile_row[(t + tile) * kTileRows + cplace] = mask ? row : kNoRow;
       }
-      top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-      const int k = std::min(90, std::max(-90, 14 - exponent_of(top)));
-      const float f = pow2i(k);
-      qsc[hb] = sc * pow2i(-k);
+      if constexpr (MASS)
+        if (lane == 0) ws.tile_item[t + tile] = item;
+      const uint32_t dst = ring_s + (q % kRing4) * kTileB;
+      const uint8_t *src = a.kv4 + (size_t)row * kRec + 16 * odd;
+#pragma unroll
+      for (int j = 0; j < kHalf / 32; ++j) {
+        cp_async16(dst + kdst + 32 * j, src + 32 * j, 16, l2_stream);
+        cp_async16(dst + vdst + ((32 * j) ^ swz), src + kHalf + 32 * j, 16, l2_stream);
+      }
+      if (kMeta == 32 || !odd) cp_async16(dst + mdst, src + 2 * kHalf, 16, l2_stream);
+    }
+    cp_async_commit();
+  };
+  uint32_t nrow, nmask;
+  {
+    uint32_t rows0[kRing4], masks0[kRing4];
+#pragma unroll
+    for (int q = 0; q < kRing4; ++q) fetch(q, rows0[q], masks0[q]);
+    fetch(kRing4, nrow, nmask);
+#pragma unroll
+    for (int q = 0; q < kRing4; ++q) issue(q, rows0[q], masks0[q]);
+  }
+  for (int q = 0; q < mt_w; ++q) {
+    cp_async_wait<kRing4 - 1>();                     // tile q
+    __syncwarp();
+    const unsigned char *kt = ring + (q % kRing4) * kTileB;
+    const unsigned char *vt = kt + kTileRows * kHalf;
+    const unsigned char *mtb = vt + kTileRows * kHalf + tq * kMeta;   // scales of row tq; rows 4 (2 j + e) further on
+
+    // ---- S: column n of half tile j is row 8 j + (n >> 1) + 4 (n & 1) -----------
+    float2 x[HB][2];                                 // [block][half tile j], .x / .y = e: head, row 8 j + 4 e + tq
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t kw[NG], mk[2][NG];                    // words; the two rows' scales and minima, bf16 pairs
+      if constexpr (NG == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(kt + (8 * j + gq) * kHalf + 16 * tq);
+        kw[0] = v.x; kw[1] = v.y; kw[2] = v.z; kw[3] = v.w;
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(kt + (8 * j + gq) * kHalf + 8 * tq);
+        kw[0] = v.x; kw[1] = v.y;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const unsigned char *p = mtb + (8 * j + 4 * e) * kMeta;
+        if constexpr (NG == 4) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(p);
+          mk[e][0] = v.x; mk[e][1] = v.y; mk[e][2] = v.z; mk[e][3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2 *>(p);
+          mk[e][0] = v.x; mk[e][1] = v.y;
+        }
+      }
+#pragma unroll
+      for (int hb = 0; hb < HB; ++hb) x[hb][j] = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        // channels (0,1) (2,3) (4,5) (6,7) -> (0,4) (1,5) (2,6) (3,7)
-        qa[g][0][hb][0] = pack_f16(bf16_lo(w[g].x) * f, bf16_lo(w[g].z) * f);
-        qa[g][0][hb][1] = pack_f16(bf16_hi(w[g].x) * f, bf16_hi(w[g].z) * f);
-        qa[g][1][hb][0] = pack_f16(bf16_lo(w[g].y) * f, bf16_lo(w[g].w) * f);
-        qa[g][1][hb][1] = pack_f16(bf16_hi(w[g].y) * f, bf16_hi(w[g].w) * f);
-        float sum = ((bf16_lo(w[g].x) + bf16_hi(w[g].x)) + (bf16_lo(w[g].y) + bf16_hi(w[g].y))) +
-                    ((bf16_lo(w[g].z) + bf16_hi(w[g].z)) + (bf16_lo(w[g].w) + bf16_hi(w[g].w)));
-        sum += __shfl_xor_sync(kFull, sum, 1);
-        sum += __shfl_xor_sync(kFull, sum, 2);
-        qs[hb][g] = sum * f;
+        // codes about 8: the accumulators start at 8 times the channels' sum
+        const float q0 = 8.0f * qs[0][g], q1 = HB == 2 ? 8.0f * qs[HB - 1][g] : 0.0f;
+        float s[4] = {q0, q0, q1, q1};
+        const uint32_t w8 = kw[g] >> 8;
+        const uint32_t b0 = low_codes(kw[g]), b1 = high_codes(kw[g]), b2 = low_codes(w8), b3 = high_codes(w8);
+        if constexpr (HB == 2) {
+          mma_f16(s, qa[g][0][0][0], qa[g][0][1][0], qa[g][0][0][1], qa[g][0][1][1], b0, b1);
+          mma_f16(s, qa[g][1][0][0], qa[g][1][1][0], qa[g][1][0][1], qa[g][1][1][1], b2, b3);
+        } else {
+          mma_f16(s, qa[g][0][0][0], 0u, qa[g][0][0][1], 0u, b0, b1);
+          mma_f16(s, qa[g][1][0][0], 0u, qa[g][1][0][1], 0u, b2, b3);
+        }
+        const float2 sg = halves(mk[0][g / 2], mk[1][g / 2], g & 1);
+        const float2 lg = halves(mk[0][NG / 2 + g / 2], mk[1][NG / 2 + g / 2], g & 1);
+#pragma unroll
+        for (int hb = 0; hb < HB; ++hb)
+          x[hb][j] = fma2(sg, make_float2(s[2 * hb], s[2 * hb + 1]),
+                          fma2(lg, make_float2(qs[hb][g], qs[hb][g]), x[hb][j]));
       }
     }
-    float m[HB], l[HB], o[HB][NG][2][4];
-    float2 olo[HB][NG];                                // two partial sums each
-    uint32_t nf[NG / 2], thr[NG / 2];                  // bf16 pairs: 2^-R_g, and the largest s it serves
+
+    // ---- values' scales, masks and softmax ------------------------------------------
+    uint32_t vs[2][2][NG / 2], vl[2][2][NG / 2];     // [half tile][e]: scales and minima, bf16 pairs
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const unsigned char *p = mtb + (8 * j + 4 * e) * kMeta + kMeta / 2;
+        if constexpr (NG == 4) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(p);
+          vs[j][e][0] = u.x; vs[j][e][1] = u.y; vl[j][e][0] = u.z; vl[j][e][1] = u.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2 *>(p);
+          vs[j][e][0] = u.x; vl[j][e][0] = u.y;
+        }
+      }
+    const uint2 mk = *reinterpret_cast<const uint2 *>(wmask + (q % kRing4) * kTileRows + 4 * tq);
+    bool over = false;
+    uint32_t smax[NG / 2];
 #pragma unroll
     for (int w = 0; w < NG / 2; ++w) {
-      nf[w] = 0x3F803F80u;
-      thr[w] = 0u;
+      smax[w] = max_bf16x2(max_bf16x2(vs[0][0][w], vs[0][1][w]), max_bf16x2(vs[1][0][w], vs[1][1][w]));
+      over |= any_gt_bf16x2(smax[w], thr[w]);
     }
 #pragma unroll
     for (int hb = 0; hb < HB; ++hb) {
-      m[hb] = -INFINITY;
-      l[hb] = 0.0f;
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        olo[hb][g] = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) o[hb][g][mt][0] = o[hb][g][mt][1] = o[hb][g][mt][2] = o[hb][g][mt][3] = 0.0f;
-      }
+      const uint32_t bit = 1u << (hd + 8 * hb);
+      x[hb][0].x = (mk.x & bit) ? x[hb][0].x * qsc[hb] : -INFINITY;
+      x[hb][0].y = (mk.x & (bit << 16)) ? x[hb][0].y * qsc[hb] : -INFINITY;
+      x[hb][1].x = (mk.y & bit) ? x[hb][1].x * qsc[hb] : -INFINITY;
+      x[hb][1].y = (mk.y & (bit << 16)) ? x[hb][1].y * qsc[hb] : -INFINITY;
+      if constexpr (MASS)
+        if (hd + 8 * hb < nh && !is_lo)
+          *reinterpret_cast<float4 *>(ws.logits + ((t + warp + (long long)q * kWarps4) * gr + hd + 8 * hb) * kTileRows +
+                                      4 * tq) = make_float4(x[hb][0].x, x[hb][0].y, x[hb][1].x, x[hb][1].y);
+      over |= fmaxf(fmaxf(x[hb][0].x, x[hb][0].y), fmaxf(x[hb][1].x, x[hb][1].y)) > m[hb] + kLazy;
     }
-
-    // ---- stream the segment's tiles: warp w takes tiles w, w + kWarps, ... -----
-    const int tiles = (r1 - r0 + kTileRows - 1) / kTileRows;
-    const int mt_w = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-    const uint32_t all = (1u << nh) - 1u;
-    const uint32_t *prow = ws.plan_row + slot0 * ap.span;
-    const uint16_t *pmask = ws.plan_mask + slot0 * ap.span;
-    const int32_t *pt = a.page_table + (long long)b * sh.max_pages;
-    int sp = 0;                                        // span of the last row fetched (rows only ascend)
-    // cache row and head mask of row lane >> 1 of tile q
-    auto fetch = [&](int q, uint32_t &row, uint32_t &mask) {
-      row = 0u;
-      mask = 0u;
-      const int gx = r0 + (warp + q * kWarps) * kTileRows + crow;
-      if (gx >= r1) return;
-      if (is_ret) {
-        while (pre[sp + 1] <= gx) ++sp;                // ends: gx < rows of the item = pre[ns_item]
-        const int e = sp * ap.span + (gx - pre[sp]);
-        row = __ldcg(prow + e);
-        mask = __ldcg(pmask + e);
-      } else {
-        const int pos = gx < loc_a ? gx : loc_w + (gx - loc_a);
-        const int page = pt[pos / kPage];
-        const bool ok = page >= 0 && page < sh.num_pages;
-        if (!ok) raise_error(a.err, SD_EBIT_PAGE);
-        row = ok ? ((uint32_t)page * sh.Hkv + g_kv) * kPage + pos % kPage : 0u;   // below 2^32 by init's check
-        mask = ok ? all : 0u;
-      }
-    };
-    // copy tile q's records; rows past the segment repeat the tile's first
-    // (finite data) and are masked out
-    auto issue = [&](int q, uint32_t row, uint32_t mask) {
-      if (q < mt_w) {
-        const int tile = warp + q * kWarps;
-        const uint32_t row0 = __shfl_sync(kFull, row, 0);
-        if (r0 + tile * kTileRows + crow >= r1) row = row0;
-        if (!odd) {
-          wmask[(q % kRing4) * kTileRows + cplace] = (uint16_t)mask;
-          if constexpr (MASS) ws.tile_row[(t + tile) * kTileRows + cplace] = mask ? row : kNoRow;
-        }
-        if constexpr (MASS)
-          if (lane == 0) ws.tile_item[t + tile] = item;
-        const uint32_t dst = ring_s + (q % kRing4) * kTileB;
-        const uint8_t *src = a.kv4 + (size_t)row * kRec + 16 * odd;
-#pragma unroll
-        for (int j = 0; j < kHalf / 32; ++j) {
-          cp_async16(dst + kdst + 32 * j, src + 32 * j, 16, l2_stream);
-          cp_async16(dst + vdst + ((32 * j) ^ swz), src + kHalf + 32 * j, 16, l2_stream);
-        }
-        if (kMeta == 32 || !odd) cp_async16(dst + mdst, src + 2 * kHalf, 16, l2_stream);
-      }
-      cp_async_commit();
-    };
-    uint32_t nrow, nmask;
-    {
-      uint32_t rows0[kRing4], masks0[kRing4];
-#pragma unroll
-      for (int q = 0; q < kRing4; ++q) fetch(q, rows0[q], masks0[q]);
-      fetch(kRing4, nrow, nmask);
-#pragma unroll
-      for (int q = 0; q < kRing4; ++q) issue(q, rows0[q], masks0[q]);
-    }
-    for (int q = 0; q < mt_w; ++q) {
-      cp_async_wait<kRing4 - 1>();                     // tile q
-      __syncwarp();
-      const unsigned char *kt = ring + (q % kRing4) * kTileB;
-      const unsigned char *vt = kt + kTileRows * kHalf;
-      const unsigned char *mtb = vt + kTileRows * kHalf + tq * kMeta;   // scales of row tq; rows 4 (2 j + e) further on
-
-      // ---- S: column n of half tile j is row 8 j + (n >> 1) + 4 (n & 1) -----------
-      float2 x[HB][2];                                 // [block][half tile j], .x / .y = e: head, row 8 j + 4 e + tq
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t kw[NG], mk[2][NG];                    // words; the two rows' scales and minima, bf16 pairs
-        if constexpr (NG == 4) {
-          const uint4 v = *reinterpret_cast<const uint4 *>(kt + (8 * j + gq) * kHalf + 16 * tq);
-          kw[0] = v.x; kw[1] = v.y; kw[2] = v.z; kw[3] = v.w;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2 *>(kt + (8 * j + gq) * kHalf + 8 * tq);
-          kw[0] = v.x; kw[1] = v.y;
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const unsigned char *p = mtb + (8 * j + 4 * e) * kMeta;
-          if constexpr (NG == 4) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(p);
-            mk[e][0] = v.x; mk[e][1] = v.y; mk[e][2] = v.z; mk[e][3] = v.w;
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2 *>(p);
-            mk[e][0] = v.x; mk[e][1] = v.y;
-          }
-        }
-#pragma unroll
-        for (int hb = 0; hb < HB; ++hb) x[hb][j] = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          // codes about 8: the accumulators start at 8 times the channels' sum
-          const float q0 = 8.0f * qs[0][g], q1 = HB == 2 ? 8.0f * qs[HB - 1][g] : 0.0f;
-          float s[4] = {q0, q0, q1, q1};
-          const uint32_t w8 = kw[g] >> 8;
-          const uint32_t b0 = low_codes(kw[g]), b1 = high_codes(kw[g]), b2 = low_codes(w8), b3 = high_codes(w8);
-          if constexpr (HB == 2) {
-            mma_f16(s, qa[g][0][0][0], qa[g][0][1][0], qa[g][0][0][1], qa[g][0][1][1], b0, b1);
-            mma_f16(s, qa[g][1][0][0], qa[g][1][1][0], qa[g][1][0][1], qa[g][1][1][1], b2, b3);
-          } else {
-            mma_f16(s, qa[g][0][0][0], 0u, qa[g][0][0][1], 0u, b0, b1);
-            mma_f16(s, qa[g][1][0][0], 0u, qa[g][1][0][1], 0u, b2, b3);
-          }
-          const float2 sg = halves(mk[0][g / 2], mk[1][g / 2], g & 1);
-          const float2 lg = halves(mk[0][NG / 2 + g / 2], mk[1][NG / 2 + g / 2], g & 1);
-#pragma unroll
-          for (int hb = 0; hb < HB; ++hb)
-            x[hb][j] = fma2(sg, make_float2(s[2 * hb], s[2 * hb + 1]),
-                            fma2(lg, make_float2(qs[hb][g], qs[hb][g]), x[hb][j]));
-        }
-      }
-
-      // ---- values' scales, masks and softmax ------------------------------------------
-      uint32_t vs[2][2][NG / 2], vl[2][2][NG / 2];     // [half tile][e]: scales and minima, bf16 pairs
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const unsigned char *p = mtb + (8 * j + 4 * e) * kMeta + kMeta / 2;
-          if constexpr (NG == 4) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(p);
-            vs[j][e][0] = u.x; vs[j][e][1] = u.y; vl[j][e][0] = u.z; vl[j][e][1] = u.w;
-          } else {
-            const uint2 u = *reinterpret_cast<const uint2 *>(p);
-            vs[j][e][0] = u.x; vl[j][e][0] = u.y;
-          }
-        }
-      const uint2 mk = *reinterpret_cast<const uint2 *>(wmask + (q % kRing4) * kTileRows + 4 * tq);
-      bool over = false;
-      uint32_t smax[NG / 2];
+    if (__any_sync(kFull, over)) {
+      // move the references: of every head to its maximum so far, of a group's
+      // scales where one outgrew it
+      float2 rf[NG / 2];                             // 2^(old R - new R) of the groups of a pair
 #pragma unroll
       for (int w = 0; w < NG / 2; ++w) {
-        smax[w] = max_bf16x2(max_bf16x2(vs[0][0][w], vs[0][1][w]), max_bf16x2(vs[1][0][w], vs[1][1][w]));
-        over |= any_gt_bf16x2(smax[w], thr[w]);
-      }
-#pragma unroll
-      for (int hb = 0; hb < HB; ++hb) {
-        const uint32_t bit = 1u << (hd + 8 * hb);
-        x[hb][0].x = (mk.x & bit) ? x[hb][0].x * qsc[hb] : -INFINITY;
-        x[hb][0].y = (mk.x & (bit << 16)) ? x[hb][0].y * qsc[hb] : -INFINITY;
-        x[hb][1].x = (mk.y & bit) ? x[hb][1].x * qsc[hb] : -INFINITY;
-        x[hb][1].y = (mk.y & (bit << 16)) ? x[hb][1].y * qsc[hb] : -INFINITY;
-        if constexpr (MASS)
-          if (hd + 8 * hb < nh && !is_lo)
-            *reinterpret_cast<float4 *>(ws.logits + ((t + warp + (long long)q * kWarps) * gr + hd + 8 * hb) * kTileRows +
-                                        4 * tq) = make_float4(x[hb][0].x, x[hb][0].y, x[hb][1].x, x[hb][1].y);
-        over |= fmaxf(fmaxf(x[hb][0].x, x[hb][0].y), fmaxf(x[hb][1].x, x[hb][1].y)) > m[hb] + kLazy;
-      }
-      if (__any_sync(kFull, over)) {
-        // move the references: of every head to its maximum so far, of a group's
-        // scales where one outgrew it
-        float2 rf[NG / 2];                             // 2^(old R - new R) of the groups of a pair
-#pragma unroll
-        for (int w = 0; w < NG / 2; ++w) {
-          uint32_t top = max_bf16x2(smax[w], __shfl_xor_sync(kFull, smax[w], 1));
-          top = max_bf16x2(top, __shfl_xor_sync(kFull, top, 2));
-          float *r = reinterpret_cast<float *>(&rf[w]);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float sv = i ? bf16_hi(top) : bf16_lo(top), lim = i ? bf16_hi(thr[w]) : bf16_lo(thr[w]);
-            const float old = i ? bf16_hi(nf[w]) : bf16_lo(nf[w]);
-            r[i] = 1.0f;
-            if (sv > lim) {
-              const int e = std::min(110, std::max(-110, exponent_of(sv)));
-              const float nn = pow2i(kScaleTop - e), nl = pow2i(e + 1);   // s 2^-R in [2^10, 2^11); serves up to 2^(e + 1)
-              r[i] = lim > 0.0f ? nn / old : 1.0f;     // powers of two: exact
-              const uint32_t keep = i ? 0x0000FFFFu : 0xFFFF0000u;
-              const uint32_t nb = __float_as_uint(nn) >> 16, lb = __float_as_uint(nl) >> 16;
-              nf[w] = (nf[w] & keep) | (i ? nb << 16 : nb);
-              thr[w] = (thr[w] & keep) | (i ? lb << 16 : lb);
-            }
-          }
-        }
-#pragma unroll
-        for (int hb = 0; hb < HB; ++hb) {
-          float top = fmaxf(fmaxf(x[hb][0].x, x[hb][0].y), fmaxf(x[hb][1].x, x[hb][1].y));
-          top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-          const float mn = fmaxf(m[hb], top);
-          const float al = mn == m[hb] ? 1.0f : fast_exp2(m[hb] - mn);   // 0 from -inf
-          m[hb] = mn;
-          l[hb] *= al;
-          const float a0 = __shfl_sync(kFull, al, 8 * tq), a1 = __shfl_sync(kFull, al, 8 * tq + 4);   // columns 2 tq, 2 tq + 1
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            olo[hb][g] = mul2(olo[hb][g], make_float2(al, al));
-            const float r = (g & 1) ? rf[g / 2].y : rf[g / 2].x;
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-              o[hb][g][mt][0] *= a0 * r;
-              o[hb][g][mt][1] *= a1 * r;
-              o[hb][g][mt][2] *= a0 * r;
-              o[hb][g][mt][3] *= a1 * r;
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int hb = 0; hb < HB; ++hb) {
-        const float mu = m[hb] == -INFINITY ? 0.0f : m[hb];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          x[hb][j].x = fast_exp2(x[hb][j].x - mu);
-          x[hb][j].y = fast_exp2(x[hb][j].y - mu);
-        }
-        l[hb] += (x[hb][0].x + x[hb][0].y) + (x[hb][1].x + x[hb][1].y);
-      }
-
-      // ---- P V -----------------------------------------------------------------------
-      uint32_t vw[2][2][NG / 2];                       // [half tile][e]: half-word pairs of groups (0,1), (2,3)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const unsigned char *p = vt + (8 * j + 4 * e + tq) * kHalf;
-          if constexpr (NG == 4) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(p + (((gq >> 1) ^ (tq & 2)) * 16) + 8 * (gq & 1));
-            vw[j][e][0] = v.x; vw[j][e][1] = v.y;
-          } else {
-            vw[j][e][0] = *reinterpret_cast<const uint32_t *>(p + 4 * gq);
-          }
-        }
-#pragma unroll
-      for (int w = 0; w < NG / 2; ++w) {
-        uint32_t vn[2][2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) vn[j][e] = mul_bf16x2(vs[j][e][w], nf[w]);   // times 2^-R: exact
+        uint32_t top = max_bf16x2(smax[w], __shfl_xor_sync(kFull, smax[w], 1));
+        top = max_bf16x2(top, __shfl_xor_sync(kFull, top, 2));
+        float *r = reinterpret_cast<float *>(&rf[w]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int g = 2 * w + i;
-          const uint32_t x0 = __byte_perm(vw[0][0][w], vw[0][1][w], i ? 0x7632 : 0x5410);
-          const uint32_t x1 = __byte_perm(vw[1][0][w], vw[1][1][w], i ? 0x7632 : 0x5410);
-          // rows gq and gq + 8 of m-tile mt: nibbles 2 mt and 2 mt + 1
-          const uint32_t A[2][4] = {{low_codes(x0), high_codes(x0), low_codes(x1), high_codes(x1)},
-                                    {low_codes(x0 >> 8), high_codes(x0 >> 8), low_codes(x1 >> 8), high_codes(x1 >> 8)}};
-#pragma unroll
-          for (int hb = 0; hb < HB; ++hb) {
-            uint32_t bh[2], bl[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float2 ps = mul2(x[hb][j], halves(vn[j][0], vn[j][1], i));
-              const float2 mid = fma2(halves(vs[j][0][w], vs[j][1][w], i), make_float2(8.0f, 8.0f),
-                                      halves(vl[j][0][w], vl[j][1][w], i));
-              olo[hb][g] = fma2(x[hb][j], mid, olo[hb][g]);
-              bh[j] = pack_f16(ps.x, ps.y);
-              const float2 h = unpack_f16(bh[j]);
-              if constexpr (PACK) {                    // lanes of the lo columns: what hi left over
-                const float2 r = fma2(lo_mul, h, ps);
-                bh[j] = pack_f16(r.x, r.y);
-              } else {
-                bl[j] = pack_f16(ps.x - h.x, ps.y - h.y);
-              }
-            }
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-              mma_f16(o[hb][g][mt], A[mt][0], A[mt][1], A[mt][2], A[mt][3], bh[0], bh[1]);
-              if constexpr (!PACK) mma_f16(o[hb][g][mt], A[mt][0], A[mt][1], A[mt][2], A[mt][3], bl[0], bl[1]);
-            }
+          const float sv = i ? bf16_hi(top) : bf16_lo(top), lim = i ? bf16_hi(thr[w]) : bf16_lo(thr[w]);
+          const float old = i ? bf16_hi(nf[w]) : bf16_lo(nf[w]);
+          r[i] = 1.0f;
+          if (sv > lim) {
+            const int e = std::min(110, std::max(-110, exponent_of(sv)));
+            const float nn = pow2i(kScaleTop - e), nl = pow2i(e + 1);   // s 2^-R in [2^10, 2^11); serves up to 2^(e + 1)
+            r[i] = lim > 0.0f ? nn / old : 1.0f;     // powers of two: exact
+            const uint32_t keep = i ? 0x0000FFFFu : 0xFFFF0000u;
+            const uint32_t nb = __float_as_uint(nn) >> 16, lb = __float_as_uint(nl) >> 16;
+            nf[w] = (nf[w] & keep) | (i ? nb << 16 : nb);
+            thr[w] = (thr[w] & keep) | (i ? lb << 16 : lb);
           }
         }
       }
-      __syncwarp();                                    // tile q and its masks read by all lanes
-      const uint32_t row = nrow, mask = nmask;
-      fetch(q + kRing4 + 1, nrow, nmask);
-      issue(q + kRing4, row, mask);
+#pragma unroll
+      for (int hb = 0; hb < HB; ++hb) {
+        float top = fmaxf(fmaxf(x[hb][0].x, x[hb][0].y), fmaxf(x[hb][1].x, x[hb][1].y));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+        const float mn = fmaxf(m[hb], top);
+        const float al = mn == m[hb] ? 1.0f : fast_exp2(m[hb] - mn);   // 0 from -inf
+        m[hb] = mn;
+        l[hb] *= al;
+        const float a0 = __shfl_sync(kFull, al, 8 * tq), a1 = __shfl_sync(kFull, al, 8 * tq + 4);   // columns 2 tq, 2 tq + 1
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          olo[hb][g] = mul2(olo[hb][g], make_float2(al, al));
+          const float r = (g & 1) ? rf[g / 2].y : rf[g / 2].x;
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            o[hb][g][mt][0] *= a0 * r;
+            o[hb][g][mt][1] *= a1 * r;
+            o[hb][g][mt][2] *= a0 * r;
+            o[hb][g][mt][3] *= a1 * r;
+          }
+        }
+      }
     }
-    cp_async_wait<0>();
+#pragma unroll
+    for (int hb = 0; hb < HB; ++hb) {
+      const float mu = m[hb] == -INFINITY ? 0.0f : m[hb];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        x[hb][j].x = fast_exp2(x[hb][j].x - mu);
+        x[hb][j].y = fast_exp2(x[hb][j].y - mu);
+      }
+      l[hb] += (x[hb][0].x + x[hb][0].y) + (x[hb][1].x + x[hb][1].y);
+    }
 
-    // ---- leave (m, l, acc) for the merge -----------------------------------------
+    // ---- P V -----------------------------------------------------------------------
+    uint32_t vw[2][2][NG / 2];                       // [half tile][e]: half-word pairs of groups (0,1), (2,3)
 #pragma unroll
-    for (int hb = 0; hb < HB; ++hb) {
-      l[hb] += __shfl_xor_sync(kFull, l[hb], 1);
-      l[hb] += __shfl_xor_sync(kFull, l[hb], 2);
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        float z = olo[hb][g].x + olo[hb][g].y;
-        z += __shfl_xor_sync(kFull, z, 1);
-        olo[hb][g].x = z + __shfl_xor_sync(kFull, z, 2);
-      }
-    }
-    __syncthreads();                                   // ring no longer read
-    float *cm = reinterpret_cast<float *>(dyn);                  // [kWarps][16]
-    float *cl = cm + kWarps * 16;                                // [kWarps][16]
-    float *cacc = cl + kWarps * 16;                              // [kWarps][GR][D]
-#pragma unroll
-    for (int hb = 0; hb < HB; ++hb) {
-      if (tq == 0 && !is_lo) {
-        cm[warp * 16 + hd + 8 * hb] = m[hb];
-        cl[warp * 16 + hd + 8 * hb] = l[hb];
+      for (int e = 0; e < 2; ++e) {
+        const unsigned char *p = vt + (8 * j + 4 * e + tq) * kHalf;
+        if constexpr (NG == 4) {
+          const uint2 v = *reinterpret_cast<const uint2 *>(p + (((gq >> 1) ^ (tq & 2)) * 16) + 8 * (gq & 1));
+          vw[j][e][0] = v.x; vw[j][e][1] = v.y;
+        } else {
+          vw[j][e][0] = *reinterpret_cast<const uint32_t *>(p + 4 * gq);
+        }
       }
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const float z0 = __shfl_sync(kFull, olo[hb][g].x, 8 * tq), z1 = __shfl_sync(kFull, olo[hb][g].x, 8 * tq + 4);
-        const float un = 1.0f / ((g & 1) ? bf16_hi(nf[g / 2]) : bf16_lo(nf[g / 2]));   // 2^R: exact
+    for (int w = 0; w < NG / 2; ++w) {
+      uint32_t vn[2][2];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          float v[4];
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] = o[hb][g][mt][e];
-            if constexpr (PACK) v[e] += __shfl_xor_sync(kFull, v[e], 2);   // hi + lo columns
+        for (int e = 0; e < 2; ++e) vn[j][e] = mul_bf16x2(vs[j][e][w], nf[w]);   // times 2^-R: exact
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int g = 2 * w + i;
+        const uint32_t x0 = __byte_perm(vw[0][0][w], vw[0][1][w], i ? 0x7632 : 0x5410);
+        const uint32_t x1 = __byte_perm(vw[1][0][w], vw[1][1][w], i ? 0x7632 : 0x5410);
+        // rows gq and gq + 8 of m-tile mt: nibbles 2 mt and 2 mt + 1
+        const uint32_t A[2][4] = {{low_codes(x0), high_codes(x0), low_codes(x1), high_codes(x1)},
+                                  {low_codes(x0 >> 8), high_codes(x0 >> 8), low_codes(x1 >> 8), high_codes(x1 >> 8)}};
+#pragma unroll
+        for (int hb = 0; hb < HB; ++hb) {
+          uint32_t bh[2], bl[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float2 ps = mul2(x[hb][j], halves(vn[j][0], vn[j][1], i));
+            const float2 mid = fma2(halves(vs[j][0][w], vs[j][1][w], i), make_float2(8.0f, 8.0f),
+                                    halves(vl[j][0][w], vl[j][1][w], i));
+            olo[hb][g] = fma2(x[hb][j], mid, olo[hb][g]);
+            bh[j] = pack_f16(ps.x, ps.y);
+            const float2 h = unpack_f16(bh[j]);
+            if constexpr (PACK) {                    // lanes of the lo columns: what hi left over
+              const float2 r = fma2(lo_mul, h, ps);
+              bh[j] = pack_f16(r.x, r.y);
+            } else {
+              bl[j] = pack_f16(ps.x - h.x, ps.y - h.y);
+            }
           }
-          if (!PACK || tq < 2) {
-            float *d0 = cacc + (warp * GR + 8 * hb + 2 * tq) * D + g * kKv4Group + 4 * gq + 2 * mt;
-            *reinterpret_cast<float2 *>(d0) = make_float2(fmaf(v[0], un, z0), fmaf(v[2], un, z0));
-            *reinterpret_cast<float2 *>(d0 + D) = make_float2(fmaf(v[1], un, z1), fmaf(v[3], un, z1));
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            mma_f16(o[hb][g][mt], A[mt][0], A[mt][1], A[mt][2], A[mt][3], bh[0], bh[1]);
+            if constexpr (!PACK) mma_f16(o[hb][g][mt], A[mt][0], A[mt][1], A[mt][2], A[mt][3], bl[0], bl[1]);
           }
         }
       }
     }
-    merge_segment<D, GR, MASS>(a, sh, ws, S, dyn, gr, c, item, first, last, b, nh);
-    t = seg_end;
-    if (tid == 0) S.item = item + 1;
+    __syncwarp();                                    // tile q and its masks read by all lanes
+    const uint32_t row = nrow, mask = nmask;
+    fetch(q + kRing4 + 1, nrow, nmask);
+    issue(q + kRing4, row, mask);
   }
+  cp_async_wait<0>();
+
+  // ---- leave (m, l, acc) for the merge -----------------------------------------
+#pragma unroll
+  for (int hb = 0; hb < HB; ++hb) {
+    l[hb] += __shfl_xor_sync(kFull, l[hb], 1);
+    l[hb] += __shfl_xor_sync(kFull, l[hb], 2);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      float z = olo[hb][g].x + olo[hb][g].y;
+      z += __shfl_xor_sync(kFull, z, 1);
+      olo[hb][g].x = z + __shfl_xor_sync(kFull, z, 2);
+    }
+  }
+  __syncthreads();                                   // ring no longer read
+  float *cm = reinterpret_cast<float *>(dyn);                  // [kWarps4][16]
+  float *cl = cm + kWarps4 * 16;                                // [kWarps4][16]
+  float *cacc = cl + kWarps4 * 16;                              // [kWarps4][GR][D]
+#pragma unroll
+  for (int hb = 0; hb < HB; ++hb) {
+    if (tq == 0 && !is_lo) {
+      cm[warp * 16 + hd + 8 * hb] = m[hb];
+      cl[warp * 16 + hd + 8 * hb] = l[hb];
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const float z0 = __shfl_sync(kFull, olo[hb][g].x, 8 * tq), z1 = __shfl_sync(kFull, olo[hb][g].x, 8 * tq + 4);
+      const float un = 1.0f / ((g & 1) ? bf16_hi(nf[g / 2]) : bf16_lo(nf[g / 2]));   // 2^R: exact
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = o[hb][g][mt][e];
+          if constexpr (PACK) v[e] += __shfl_xor_sync(kFull, v[e], 2);   // hi + lo columns
+        }
+        if (!PACK || tq < 2) {
+          float *d0 = cacc + (warp * GR + 8 * hb + 2 * tq) * D + g * kKv4Group + 4 * gq + 2 * mt;
+          *reinterpret_cast<float2 *>(d0) = make_float2(fmaf(v[0], un, z0), fmaf(v[2], un, z0));
+          *reinterpret_cast<float2 *>(d0 + D) = make_float2(fmaf(v[1], un, z1), fmaf(v[3], un, z1));
+        }
+      }
+    }
+  }
+  merge_segment<D, GR, MASS, kWarps4>(a, sh, ws, S, dyn, gr, blockIdx.x, item, first, last, first, b, nh);
 }
 
+// Shared memory and resident CTAs of one instantiation; with `launch`, the launch
+// (as many CTAs as the layout can hand out).
 template <int D, int GR, bool MASS>
-cudaError_t launch_t(const AttendArgs &a, const Shape &sh, const Tables &tb, const AttParams &p, const AttWs &ws,
-                     int gr, cudaStream_t st) {
-  const size_t ring = (size_t)kWarps * kRing4 * kTileRows * kv4_record_bytes(D);
-  const size_t lists = (size_t)kWarps * kRing4 * kTileRows * 2 + (size_t)(p.ns + 1) * 4;
-  const size_t merge = std::max((size_t)kWarps * 32 * 4 + (size_t)kWarps * GR * D * 4,
+cudaError_t config_t(const AttendArgs *launch, const Shape &sh, const Tables &tb, const AttParams &p, const AttWs *ws,
+                     int gr, cudaStream_t st, int *grid) {
+  const size_t ring = (size_t)kWarps4 * kRing4 * kTileRows * kv4_record_bytes(D);
+  const size_t lists = (size_t)kWarps4 * kRing4 * kTileRows * 2 + (size_t)(p.ns + 1) * 4;
+  const size_t merge = std::max((size_t)kWarps4 * 32 * 4 + (size_t)kWarps4 * GR * D * 4,
                                 (size_t)GR * (kMergeChunk + 2) * 4);
   const size_t bytes = std::max(ring + lists, merge);
-  const cudaError_t e = set_smem(attend_kv4_kernel<D, GR, MASS>, bytes);
+  cudaError_t e = set_smem(attend_kv4_kernel<D, GR, MASS>, bytes);
   if (e != cudaSuccess) return e;
-  const int grid = resident_ctas(attend_kv4_kernel<D, GR, MASS>, kThreads, bytes);
-  if (grid <= 0) return cudaErrorInvalidConfiguration;
-  return launch_pdl(attend_kv4_kernel<D, GR, MASS>, dim3(grid), dim3(kThreads), bytes, st, 0, a, sh, tb, p, ws, gr);
+  *grid = std::min(kMaxSegments, resident_ctas(attend_kv4_kernel<D, GR, MASS>, kThreads4, bytes));
+  if (!launch) return cudaSuccess;
+  if (*grid <= 0) return cudaErrorInvalidConfiguration;
+  // the layout's bound on the shares (item_segments)
+  const int waves = std::max(1, (2 * p.ni + *grid - 1) / *grid);
+  const int ctas = (int)std::max<long long>(std::min<long long>((long long)*grid * waves, kMaxSegments), p.ni + 1);
+  return launch_pdl(attend_kv4_kernel<D, GR, MASS>, dim3(ctas), dim3(kThreads4), bytes, st, 0, *launch, sh, tb, p, *ws, gr);
 }
 
-template <int D, int GR>
-cudaError_t launch_m(const AttendArgs &a, const Shape &sh, const Tables &tb, const AttParams &p, const AttWs &ws,
-                     int gr, cudaStream_t st) {
-  return a.mass ? launch_t<D, GR, true>(a, sh, tb, p, ws, gr, st) : launch_t<D, GR, false>(a, sh, tb, p, ws, gr, st);
+template <int D, bool MASS>
+cudaError_t config_d(const AttendArgs *launch, const Shape &sh, const Tables &tb, const AttParams &p, const AttWs *ws,
+                     int gr, cudaStream_t st, int *grid) {
+  if (gr <= 4) return config_t<D, 4, MASS>(launch, sh, tb, p, ws, gr, st, grid);
+  if (gr <= 8) return config_t<D, 8, MASS>(launch, sh, tb, p, ws, gr, st, grid);
+  return config_t<D, 16, MASS>(launch, sh, tb, p, ws, gr, st, grid);
 }
 
-template <int D>
-cudaError_t launch_d(const AttendArgs &a, const Shape &sh, const Tables &tb, const AttParams &p, const AttWs &ws,
-                     int gr, cudaStream_t st) {
-  if (gr <= 4) return launch_m<D, 4>(a, sh, tb, p, ws, gr, st);
-  if (gr <= 8) return launch_m<D, 8>(a, sh, tb, p, ws, gr, st);
-  return launch_m<D, 16>(a, sh, tb, p, ws, gr, st);
+cudaError_t config(const AttendArgs *launch, const Shape &sh, const Tables &tb, const AttParams &p, const AttWs *ws,
+                   int gr, bool mass, cudaStream_t st, int *grid) {
+  if (sh.d == 128)
+    return mass ? config_d<128, true>(launch, sh, tb, p, ws, gr, st, grid)
+                : config_d<128, false>(launch, sh, tb, p, ws, gr, st, grid);
+  return mass ? config_d<64, true>(launch, sh, tb, p, ws, gr, st, grid)
+              : config_d<64, false>(launch, sh, tb, p, ws, gr, st, grid);
 }
 
 }  // namespace
 
+int kv4_main_grid(const Shape &sh, const Tables &tb, const AttParams &p, int gr, bool mass) {
+  int grid = 0;
+  return config(nullptr, sh, tb, p, nullptr, gr, mass, nullptr, &grid) == cudaSuccess ? grid : 0;
+}
+
 cudaError_t launch_attend_kv4_main(const AttendArgs &a, const Shape &sh, const Tables &tb, const AttParams &p,
                                    const AttWs &ws, int gr, cudaStream_t st) {
-  return sh.d == 128 ? launch_d<128>(a, sh, tb, p, ws, gr, st) : launch_d<64>(a, sh, tb, p, ws, gr, st);
+  int grid = 0;
+  return config(&a, sh, tb, p, &ws, gr, a.mass != nullptr, st, &grid);
 }
 
 }  // namespace sd
