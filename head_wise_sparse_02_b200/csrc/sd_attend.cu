@@ -119,70 +119,149 @@ __device__ void item_prefix(const AttendArgs &a, const Shape &sh, const Tables &
   if (tid == 0) ws.tstart[ap.ni] = carry;
 }
 
-// Shares for a main kernel whose CTAs take one item each, by the layout's CTA
-// after item_prefix: item i of t_i tiles gets ceil(t_i / per) CTAs, each an equal
-// part of it, with `per` just large enough that all fit the grid.  `grid` CTAs
-// are resident at once; many items take several times that, so that an item of
-// average size still has more than one CTA.
+// Shares for a main kernel whose CTAs take one item each: item i of t_i tiles
+// gets ceil(t_i / per) CTAs, each an equal part of it, with `per` just large
+// enough that all fit the grid.  `grid` CTAs are resident at once; many items take
+// several times that, so that an item of average size still has more than one CTA.
 constexpr int kMinSegTiles = 8;         // tiles a CTA takes at least (two per warp) before an item gets another
-constexpr int kLayoutItems = 2048;      // items whose first CTAs are searched in shared memory
 
+template <typename T>
+__device__ __forceinline__ T tiles_per_segment(T W, int ni, int grid) {
+  const int waves = (2 * ni + grid - 1) / grid;
+  int slots = grid * (waves > 1 ? waves : 1);
+  if (slots > kMaxSegments) slots = kMaxSegments;
+  const T room = slots > ni ? slots - ni : 1;
+  const T per = (W + room - 1) / room;
+  return per > kMinSegTiles ? per : T(kMinSegTiles);
+}
+
+// CTA c's share: of the item whose CTAs start at first(i) (ascending), with its
+// tiles starting at tstart(i)
+template <typename First, typename Tile, typename Rows>
+__device__ __forceinline__ Segment segment_of(int c, int ni, First first, Tile tstart, Rows rows) {
+  int lo = 0, hi = ni;                                 // last item with first(lo) <= c
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first(mid) <= c) lo = mid;
+    else hi = mid;
+  }
+  const int c0 = first(lo);
+  const uint32_t n = first(lo + 1) - c0, k = c - c0;
+  const long long t0 = tstart(lo);
+  // t tiles (below 2^21), the first t % n CTAs take one more than the others
+  const uint32_t t = (uint32_t)(tstart(lo + 1) - t0), each = t / n, more = t - each * n;
+  const uint32_t a0 = each * k + std::min(k, more);
+  return Segment{lo, (int)a0, (int)(each + (k < more)), c0, c0 + (int)n - 1, rows(lo), t0 + a0};
+}
+
+// Exclusive prefix sums of one value per thread over the block (whole warps), and their total
+template <typename T>
+__device__ __forceinline__ T block_prefix(T v, T *wsum, T &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  T w = lane < (int)(blockDim.x >> 5) ? wsum[lane] : T(0);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(kFull, w, o);
+    if (lane >= o) w += y;
+  }
+  total = __shfl_sync(kFull, w, 31);
+  const T before = __shfl_sync(kFull, w, warp > 0 ? warp - 1 : 0);
+  __syncthreads();                                     // wsum is free again
+  return (warp > 0 ? before : T(0)) + incl - v;
+}
+
+// Shares of any number of items, after item_prefix (global memory throughout)
 __device__ void item_segments(const AttParams &ap, const AttWs &ws, int grid) {
-  __shared__ int cs[kLayoutItems + 1];
   __shared__ int wsum[32];
-  __shared__ int carry;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  const int tid = threadIdx.x;
   __syncthreads();
-  const long long W = ws.tstart[ap.ni];
-  const int waves = (2 * ap.ni + grid - 1) / grid;
-  const long long room = std::max<long long>(std::min<long long>((long long)grid * std::max(1, waves), kMaxSegments) - ap.ni, 1);
-  const long long per = std::max<long long>(kMinSegTiles, (W + room - 1) / room);
-  const bool small = ap.ni <= kLayoutItems;
-  if (tid == 0) carry = 0;
-  __syncthreads();
+  const long long per = tiles_per_segment<long long>(ws.tstart[ap.ni], ap.ni, grid);
+  int carry = 0;
   for (int base = 0; base < ap.ni; base += blockDim.x) {
     const int i = base + tid;
     const int n = i < ap.ni ? (int)((ws.tstart[i + 1] - ws.tstart[i] + per - 1) / per) : 0;
-    int incl = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kFull, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    int before = carry, total = 0;
-    for (int w = 0; w < nw; ++w) {
-      if (w < warp) before += wsum[w];
-      total += wsum[w];
-    }
-    if (i < ap.ni) {
-      if (small) cs[i] = before + incl - n;
-      else ws.cstart[i] = before + incl - n;
-    }
-    __syncthreads();
-    if (tid == 0) carry += total;
-    __syncthreads();
+    int total;
+    const int at = block_prefix<int>(n, wsum, total);
+    if (i < ap.ni) ws.cstart[i] = carry + at;
+    carry += total;
   }
-  const int ns = carry;
   if (tid == 0) {
-    ws.n_seg[0] = ns;
-    if (small) cs[ap.ni] = ns;
-    else ws.cstart[ap.ni] = ns;
+    ws.n_seg[0] = carry;
+    ws.cstart[ap.ni] = carry;
   }
   __syncthreads();
-  const int *first = small ? cs : ws.cstart;
-  for (int c = tid; c < ns; c += blockDim.x) {
-    int lo = 0, hi = ap.ni;                            // last item with first[lo] <= c
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (first[mid] <= c) lo = mid;
-      else hi = mid;
+  for (int c = tid; c < carry; c += blockDim.x)
+    ws.seg[c] = segment_of(c, ap.ni, [&](int i) { return ws.cstart[i]; }, [&](int i) { return ws.tstart[i]; },
+                           [&](int i) { return ws.item_rows[i]; });
+}
+
+// item_prefix and item_segments when the block has a thread per item (at most
+// 1024): the span counts are loaded before the lengths that say which of them
+// count, and everything that is read again stays in shared memory.  The whole
+// call waits for this one CTA, so it has no more warps than the items need
+// (7.3 us as two passes over global memory by 1024 threads).
+template <int D>
+__device__ void item_layout(const AttendArgs &a, const Shape &sh, const Tables &tb, const AttParams &ap,
+                            const AttWs &ws, int seg_grid) {
+  __shared__ int rows[1024], spans[1024], first[1025];
+  __shared__ uint32_t tstart[1025], wsum[32];          // at most 1024 items of 2^21 tiles
+  const int tid = threadIdx.x;
+  const int entries = ap.n_ret_items * ap.ns;
+  int cnt = tid < entries ? __ldcg(ws.plan_cnt + tid) : 0;
+  if (tid < ap.ni) {
+    const bool is_ret = tid < ap.n_ret_items;
+    const int b = is_ret ? tid / tb.n_ret : (tid - ap.n_ret_items) / tb.n_loc;
+    const long long N0 = a.seq_lens[b];
+    if (N0 < 0 || N0 > sh.max_len) raise_error(a.err, SD_EBIT_SEQLEN);
+    const int N = (int)clamp_len(a, sh, b);
+    const int la = std::min(a.num_sinks, N), lw = std::max(la, N - std::min(a.window, N));
+    spans[tid] = is_ret ? (N + ap.span - 1) / ap.span : 0;
+    rows[tid] = is_ret ? 0 : la + (N - lw);
+  }
+  __syncthreads();
+  for (int e = tid; e < entries; e += blockDim.x) {
+    if (e != tid) cnt = __ldcg(ws.plan_cnt + e);
+    const int i = e / ap.ns;
+    if (e - i * ap.ns < spans[i] && cnt) atomicAdd(&rows[i], cnt);
+  }
+  __syncthreads();
+  const int n_rows = tid < ap.ni ? rows[tid] : 0;
+  const uint32_t nt = (uint32_t)(n_rows + kTileRows - 1) / kTileRows;
+  uint32_t W;
+  const uint32_t at = block_prefix<uint32_t>(nt, wsum, W);
+  if (tid < ap.ni) {
+    ws.tstart[tid] = tstart[tid] = at;
+    ws.item_rows[tid] = n_rows;
+    ws.tickets[tid] = 0u;
+  }
+  if (tid == 0) ws.tstart[ap.ni] = tstart[ap.ni] = W;
+  if (seg_grid > 0) {
+    const uint32_t per = tiles_per_segment<uint32_t>(W, ap.ni, seg_grid);
+    uint32_t total;
+    const uint32_t c0 = block_prefix<uint32_t>((nt + per - 1) / per, wsum, total);
+    if (tid < ap.ni) first[tid] = (int)c0;
+    if (tid == 0) {
+      first[ap.ni] = (int)total;
+      ws.n_seg[0] = (int)total;
     }
-    const int c0 = first[lo], n = first[lo + 1] - c0;
-    const long long t0 = ws.tstart[lo], t = ws.tstart[lo + 1] - t0;
-    const int a0 = (int)(t * (c - c0) / n), a1 = (int)(t * (c - c0 + 1) / n);
-    ws.seg[c] = Segment{lo, a0, a1 - a0, c0, c0 + n - 1, ws.item_rows[lo], t0 + a0};
+    __syncthreads();
+    for (int c = tid; c < (int)total; c += blockDim.x)
+      ws.seg[c] = segment_of(c, ap.ni, [&](int i) { return first[i]; }, [&](int i) { return tstart[i]; },
+                             [&](int i) { return rows[i]; });
+  }
+  if (tid < ap.ni && n_rows == 0) {                    // no main CTA visits the item
+    int b;
+    bool is_ret;
+    const Group &grp = item_group(tb, ap, tid, b, is_ret);
+    for (int x = 0; x < grp.n * D; ++x) a.out[((long long)b * sh.Hq + grp.q_head[x / D]) * D + x % D] = 0.0f;
   }
 }
 
@@ -194,6 +273,10 @@ attend_prefix_kernel(const AttendArgs a, const Shape sh, const Tables tb, const 
                      int seg_grid) {
   pdl_wait();
   pdl_trigger();
+  if (ap.ni <= (int)blockDim.x) {
+    item_layout<D>(a, sh, tb, ap, ws, seg_grid);
+    return;
+  }
   item_prefix<D>(a, sh, tb, ap, ws);
   if (seg_grid > 0) item_segments(ap, ws, seg_grid);
 }
@@ -218,6 +301,16 @@ __device__ void plan_span(const AttendArgs &a, const Shape &sh, const Tables &tb
     if (tid == 0) ws.plan_cnt[slot] = 0;
     return;
   }
+  for (int o = tid; o < nh * bwords; o += kPlanThreads) hbm[o] = 0u;
+  {
+    const int32_t *pt = a.page_table + (long long)b * sh.max_pages + p0 / kPage;
+    const int npg = (int)((p1 - p0 + kPage - 1) / kPage);
+#pragma unroll 4
+    for (int o = tid; o < npg; o += kPlanThreads) {
+      const int page = pt[o];
+      pslice[o] = (page >= 0 && page < sh.num_pages) ? page : -1;
+    }
+  }
   // one search per warp: (head, bound) pairs, lower bounds of p0 and p1
   for (int t = warp; t < 2 * nh; t += kPlanWarps) {
     const int i = t >> 1;
@@ -231,15 +324,6 @@ __device__ void plan_span(const AttendArgs &a, const Shape &sh, const Tables &tb
     const int at = warp_lower_bound<int32_t>(sel, (int)c, (int32_t)((t & 1) ? p1 : p0), lane);
     if (lane == 0) ((t & 1) ? seg_hi : seg_lo)[i] = at;
   }
-  for (int o = tid; o < nh * bwords; o += kPlanThreads) hbm[o] = 0u;
-  {
-    const int32_t *pt = a.page_table + (long long)b * sh.max_pages + p0 / kPage;
-    const int npg = (int)((p1 - p0 + kPage - 1) / kPage);
-    for (int o = tid; o < npg; o += kPlanThreads) {
-      const int page = pt[o];
-      pslice[o] = (page >= 0 && page < sh.num_pages) ? page : -1;
-    }
-  }
   __syncthreads();
   if (tid == 0) {                                    // where each head's entries start in one flat range
     int run = 0;
@@ -251,7 +335,7 @@ __device__ void plan_span(const AttendArgs &a, const Shape &sh, const Tables &tb
   }
   __syncthreads();
   // all heads' entries of the span in one flat loop, so that their loads overlap
-#pragma unroll 4
+#pragma unroll 8
   for (int x = tid; x < seg_at[nh]; x += kPlanThreads) {
     int i = 0;
     while (seg_at[i + 1] <= x) ++i;
@@ -841,7 +925,8 @@ cudaError_t launch_t(const AttendArgs &a, const Shape &sh, const Tables &tb, con
   }
   const int seg_grid = a.kv4 ? kv4_main_grid(sh, tb, p, GR, a.mass != nullptr) : 0;
   if (a.kv4 && seg_grid <= 0) return cudaErrorInvalidConfiguration;
-  e = launch_pdl(attend_prefix_kernel<D>, dim3(1), dim3(1024), 0, st, 0, a, sh, tb, p, ws, seg_grid);
+  e = launch_pdl(attend_prefix_kernel<D>, dim3(1), dim3(std::min(1024, std::max(128, pow2_ceil(p.ni)))), 0, st, 0, a, sh, tb, p, ws,
+                 seg_grid);
   if (e != cudaSuccess) return e;
   if (a.kv4)
     e = launch_attend_kv4_main(a, sh, tb, p, ws, GR, st);
