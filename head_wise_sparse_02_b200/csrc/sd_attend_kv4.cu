@@ -31,10 +31,13 @@
 // Per warp, a 16-row tile (16 records):
 //   S    heads on M, rows on N (mma.m16n8k16, B = key codes), so the scores leave
 //        in the layout that P V wants for B;
-//   P V  channels on M (A = value codes), heads on N.  With at most four heads,
-//        columns 0-3 carry the hi terms and 4-7 the lo terms of the same heads:
-//        half the MMAs.  Column n of S is row (n >> 1) + 4 (n & 1) of its half
-//        tile, which spreads the value loads over the banks.
+//   P V  channels on M (A = value codes), heads on N.
+// Column n of S is row (n >> 1) + 4 (n & 1) of its half tile, which spreads the
+// value loads over the banks.  With at most four heads nothing is done twice for
+// the unused rows and columns: rows 0-3 of S take the first half tile and rows
+// 4-7 the second (two products into one accumulator, each with zeros for the
+// other's queries), so a lane scales and weighs two rows instead of four, and
+// columns 0-3 of P V carry the hi terms and 4-7 the lo terms, half the products.
 #include "sd_attend.cuh"
 
 namespace sd {
@@ -64,6 +67,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d = a * b: the same with nothing to add to
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 // two floats -> f16x2 (x in the low half), round to nearest even
 __device__ __forceinline__ uint32_t pack_f16(float x, float y) {
@@ -121,7 +131,7 @@ __device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_ui
 //                        [span prefix of the current item: ns + 1 ints]
 // between items the ring holds the warps' (m, l, acc) for the CTA merge
 template <int D, int GR, bool MASS>
-__global__ void __launch_bounds__(kThreads4, GR > 8 ? 2 : 4)
+__global__ void __launch_bounds__(kThreads4, GR > 8 ? 2 : 3)
 attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const AttParams ap, const AttWs ws, int gr) {
   constexpr int NG = D / kKv4Group;                  // groups of channels
   constexpr int kRec = kv4_record_bytes(D);
@@ -188,8 +198,9 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
   const uint32_t mdst = 2 * kTileRows * kHalf + crow * kMeta + 16 * odd;
   const float sc = a.attn_scale * kLog2e;
   const uint64_t l2_stream = evict_first_policy();
-  const bool is_lo = PACK && gq >= 4;
-  const float2 lo_mul = is_lo ? make_float2(-1.0f, -1.0f) : make_float2(0.0f, 0.0f);
+  constexpr int NJ = PACK ? 1 : 2;                   // half tiles a lane weighs
+  const bool upper = PACK && gq >= 4;                // the lane's half tile, and its columns of P V: lo terms
+  const int half = upper ? 1 : 0;
   const int hd = PACK ? (gq & 3) : gq;               // head (of column block 0) whose scores this lane holds
 
   __syncthreads();
@@ -201,7 +212,10 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
   // ---- queries: A fragments (heads on M; k = the channels of the record's
   // words: lane tq holds channels 8 tq .. 8 tq + 7 of every group, nibble pairs
   // (i, i + 4)), and the sums over the groups' channels; all times 2^k
-  uint32_t qa[NG][2][HB][2];
+  // With at most four heads [.][0] and [.][1] are the queries of rows 0-3 and of
+  // rows 4-7, zero in the others.
+  constexpr int QB = PACK ? 2 : HB;
+  uint32_t qa[NG][2][QB][2];
   float qs[HB][NG], qsc[HB];
 #pragma unroll
   for (int hb = 0; hb < HB; ++hb) {
@@ -234,10 +248,18 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
       sum += __shfl_xor_sync(kFull, sum, 1);
       sum += __shfl_xor_sync(kFull, sum, 2);
       qs[hb][g] = sum * f;
+      if constexpr (PACK)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            qa[g][ks][1][i] = upper ? qa[g][ks][0][i] : 0u;
+            qa[g][ks][0][i] = upper ? 0u : qa[g][ks][0][i];
+          }
     }
   }
   float m[HB], l[HB], o[HB][NG][2][4];
-  float2 olo[HB][NG];                                // two partial sums each
+  float2 olo[HB][NG], oup[HB][NG];                   // sums of p lo and of 8 p s 2^-R, two partial sums each
   uint32_t nf[NG / 2], thr[NG / 2];                  // bf16 pairs: 2^-R_g, and the largest s it serves
 #pragma unroll
   for (int w = 0; w < NG / 2; ++w) {
@@ -250,7 +272,7 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
     l[hb] = 0.0f;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      olo[hb][g] = make_float2(0.0f, 0.0f);
+      olo[hb][g] = oup[hb][g] = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) o[hb][g][mt][0] = o[hb][g][mt][1] = o[hb][g][mt][2] = o[hb][g][mt][3] = 0.0f;
     }
@@ -325,17 +347,22 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
     const unsigned char *mtb = vt + kTileRows * kHalf + tq * kMeta;   // scales of row tq; rows 4 (2 j + e) further on
 
     // ---- S: column n of half tile j is row 8 j + (n >> 1) + 4 (n & 1) -----------
-    float2 x[HB][2];                                 // [block][half tile j], .x / .y = e: head, row 8 j + 4 e + tq
+    float2 x[HB][NJ];                                // [block][half tile], .x / .y = e: head, row 8 j + 4 e + tq
+    uint32_t kw[2][NG];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      uint32_t kw[NG], mk[2][NG];                    // words; the two rows' scales and minima, bf16 pairs
       if constexpr (NG == 4) {
         const uint4 v = *reinterpret_cast<const uint4 *>(kt + (8 * j + gq) * kHalf + 16 * tq);
-        kw[0] = v.x; kw[1] = v.y; kw[2] = v.z; kw[3] = v.w;
+        kw[j][0] = v.x; kw[j][1] = v.y; kw[j][2] = v.z; kw[j][3] = v.w;
       } else {
         const uint2 v = *reinterpret_cast<const uint2 *>(kt + (8 * j + gq) * kHalf + 8 * tq);
-        kw[0] = v.x; kw[1] = v.y;
+        kw[j][0] = v.x; kw[j][1] = v.y;
       }
+    }
+#pragma unroll
+    for (int jj = 0; jj < NJ; ++jj) {
+      const int j = PACK ? half : jj;
+      uint32_t mk[2][NG];                            // the two rows' scales and minima, bf16 pairs
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const unsigned char *p = mtb + (8 * j + 4 * e) * kMeta;
@@ -348,84 +375,92 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
         }
       }
 #pragma unroll
-      for (int hb = 0; hb < HB; ++hb) x[hb][j] = make_float2(0.0f, 0.0f);
+      for (int hb = 0; hb < HB; ++hb) x[hb][jj] = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        // codes about 8: the accumulators start at 8 times the channels' sum
-        const float q0 = 8.0f * qs[0][g], q1 = HB == 2 ? 8.0f * qs[HB - 1][g] : 0.0f;
-        float s[4] = {q0, q0, q1, q1};
-        const uint32_t w8 = kw[g] >> 8;
-        const uint32_t b0 = low_codes(kw[g]), b1 = high_codes(kw[g]), b2 = low_codes(w8), b3 = high_codes(w8);
-        if constexpr (HB == 2) {
-          mma_f16(s, qa[g][0][0][0], qa[g][0][1][0], qa[g][0][0][1], qa[g][0][1][1], b0, b1);
-          mma_f16(s, qa[g][1][0][0], qa[g][1][1][0], qa[g][1][0][1], qa[g][1][1][1], b2, b3);
-        } else {
-          mma_f16(s, qa[g][0][0][0], 0u, qa[g][0][0][1], 0u, b0, b1);
-          mma_f16(s, qa[g][1][0][0], 0u, qa[g][1][0][1], 0u, b2, b3);
+        float s[4];
+#pragma unroll
+        for (int u = 0; u < (PACK ? 2 : 1); ++u) {
+          const uint32_t w = kw[PACK ? u : jj][g], w8 = w >> 8;
+          const uint32_t b0 = low_codes(w), b1 = high_codes(w), b2 = low_codes(w8), b3 = high_codes(w8);
+          const uint32_t a1 = HB == 2 ? qa[g][0][QB - 1][0] : 0u, a3 = HB == 2 ? qa[g][0][QB - 1][1] : 0u;
+          const uint32_t c1 = HB == 2 ? qa[g][1][QB - 1][0] : 0u, c3 = HB == 2 ? qa[g][1][QB - 1][1] : 0u;
+          if (u == 0) mma_f16_first(s, qa[g][0][u][0], a1, qa[g][0][u][1], a3, b0, b1);
+          else mma_f16(s, qa[g][0][u][0], a1, qa[g][0][u][1], a3, b0, b1);
+          mma_f16(s, qa[g][1][u][0], c1, qa[g][1][u][1], c3, b2, b3);
         }
+        // codes were about 8: 8 times the channels' sum joins here
         const float2 sg = halves(mk[0][g / 2], mk[1][g / 2], g & 1);
         const float2 lg = halves(mk[0][NG / 2 + g / 2], mk[1][NG / 2 + g / 2], g & 1);
 #pragma unroll
-        for (int hb = 0; hb < HB; ++hb)
-          x[hb][j] = fma2(sg, make_float2(s[2 * hb], s[2 * hb + 1]),
-                          fma2(lg, make_float2(qs[hb][g], qs[hb][g]), x[hb][j]));
+        for (int hb = 0; hb < HB; ++hb) {
+          const float2 q1 = make_float2(qs[hb][g], qs[hb][g]);
+          const float2 up = fma2(q1, make_float2(8.0f, 8.0f), make_float2(s[2 * hb], s[2 * hb + 1]));
+          x[hb][jj] = fma2(sg, up, fma2(lg, q1, x[hb][jj]));
+        }
       }
     }
 
     // ---- values' scales, masks and softmax ------------------------------------------
-    uint32_t vs[2][2][NG / 2], vl[2][2][NG / 2];     // [half tile][e]: scales and minima, bf16 pairs
+    uint32_t vs[NJ][2][NG / 2], vl[NJ][2][NG / 2];   // [half tile][e]: scales and minima, bf16 pairs
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int jj = 0; jj < NJ; ++jj)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const unsigned char *p = mtb + (8 * j + 4 * e) * kMeta + kMeta / 2;
+        const unsigned char *p = mtb + (8 * (PACK ? half : jj) + 4 * e) * kMeta + kMeta / 2;
         if constexpr (NG == 4) {
           const uint4 u = *reinterpret_cast<const uint4 *>(p);
-          vs[j][e][0] = u.x; vs[j][e][1] = u.y; vl[j][e][0] = u.z; vl[j][e][1] = u.w;
+          vs[jj][e][0] = u.x; vs[jj][e][1] = u.y; vl[jj][e][0] = u.z; vl[jj][e][1] = u.w;
         } else {
           const uint2 u = *reinterpret_cast<const uint2 *>(p);
-          vs[j][e][0] = u.x; vl[j][e][0] = u.y;
+          vs[jj][e][0] = u.x; vl[jj][e][0] = u.y;
         }
       }
-    const uint2 mk = *reinterpret_cast<const uint2 *>(wmask + (q % kRing4) * kTileRows + 4 * tq);
     bool over = false;
     uint32_t smax[NG / 2];
 #pragma unroll
     for (int w = 0; w < NG / 2; ++w) {
-      smax[w] = max_bf16x2(max_bf16x2(vs[0][0][w], vs[0][1][w]), max_bf16x2(vs[1][0][w], vs[1][1][w]));
+      smax[w] = max_bf16x2(vs[0][0][w], vs[0][1][w]);
+      if constexpr (!PACK) smax[w] = max_bf16x2(smax[w], max_bf16x2(vs[NJ - 1][0][w], vs[NJ - 1][1][w]));
       over |= any_gt_bf16x2(smax[w], thr[w]);
     }
+    float top[HB];                                   // the lane's largest logit
 #pragma unroll
     for (int hb = 0; hb < HB; ++hb) {
       const uint32_t bit = 1u << (hd + 8 * hb);
-      x[hb][0].x = (mk.x & bit) ? x[hb][0].x * qsc[hb] : -INFINITY;
-      x[hb][0].y = (mk.x & (bit << 16)) ? x[hb][0].y * qsc[hb] : -INFINITY;
-      x[hb][1].x = (mk.y & bit) ? x[hb][1].x * qsc[hb] : -INFINITY;
-      x[hb][1].y = (mk.y & (bit << 16)) ? x[hb][1].y * qsc[hb] : -INFINITY;
-      if constexpr (MASS)
-        if (hd + 8 * hb < nh && !is_lo)
-          *reinterpret_cast<float4 *>(ws.logits + ((t + warp + (long long)q * kWarps4) * gr + hd + 8 * hb) * kTileRows +
-                                      4 * tq) = make_float4(x[hb][0].x, x[hb][0].y, x[hb][1].x, x[hb][1].y);
-      over |= fmaxf(fmaxf(x[hb][0].x, x[hb][0].y), fmaxf(x[hb][1].x, x[hb][1].y)) > m[hb] + kLazy;
+      top[hb] = -INFINITY;
+#pragma unroll
+      for (int jj = 0; jj < NJ; ++jj) {
+        const int j = PACK ? half : jj;
+        const uint32_t mk = *reinterpret_cast<const uint32_t *>(wmask + (q % kRing4) * kTileRows + 4 * tq + 2 * j);
+        x[hb][jj].x = (mk & bit) ? x[hb][jj].x * qsc[hb] : -INFINITY;
+        x[hb][jj].y = (mk & (bit << 16)) ? x[hb][jj].y * qsc[hb] : -INFINITY;
+        top[hb] = fmaxf(top[hb], fmaxf(x[hb][jj].x, x[hb][jj].y));
+        if constexpr (MASS)
+          if (hd + 8 * hb < nh)
+            *reinterpret_cast<float2 *>(ws.logits + ((t + warp + (long long)q * kWarps4) * gr + hd + 8 * hb) * kTileRows +
+                                        4 * tq + 2 * j) = x[hb][jj];
+      }
+      over |= top[hb] > m[hb] + kLazy;
     }
     if (__any_sync(kFull, over)) {
       // move the references: of every head to its maximum so far, of a group's
       // scales where one outgrew it
-      float2 rf[NG / 2];                             // 2^(old R - new R) of the groups of a pair
+      float rf[NG];                                  // 2^(old R - new R)
 #pragma unroll
       for (int w = 0; w < NG / 2; ++w) {
-        uint32_t top = max_bf16x2(smax[w], __shfl_xor_sync(kFull, smax[w], 1));
-        top = max_bf16x2(top, __shfl_xor_sync(kFull, top, 2));
-        float *r = reinterpret_cast<float *>(&rf[w]);
+        uint32_t top_s = max_bf16x2(smax[w], __shfl_xor_sync(kFull, smax[w], 1));
+        top_s = max_bf16x2(top_s, __shfl_xor_sync(kFull, top_s, 2));
+        if constexpr (PACK) top_s = max_bf16x2(top_s, __shfl_xor_sync(kFull, top_s, 16));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float sv = i ? bf16_hi(top) : bf16_lo(top), lim = i ? bf16_hi(thr[w]) : bf16_lo(thr[w]);
+          const float sv = i ? bf16_hi(top_s) : bf16_lo(top_s), lim = i ? bf16_hi(thr[w]) : bf16_lo(thr[w]);
           const float old = i ? bf16_hi(nf[w]) : bf16_lo(nf[w]);
-          r[i] = 1.0f;
+          rf[2 * w + i] = 1.0f;
           if (sv > lim) {
             const int e = std::min(110, std::max(-110, exponent_of(sv)));
             const float nn = pow2i(kScaleTop - e), nl = pow2i(e + 1);   // s 2^-R in [2^10, 2^11); serves up to 2^(e + 1)
-            r[i] = lim > 0.0f ? nn / old : 1.0f;     // powers of two: exact
+            rf[2 * w + i] = lim > 0.0f ? nn / old : 1.0f;     // powers of two: exact
             const uint32_t keep = i ? 0x0000FFFFu : 0xFFFF0000u;
             const uint32_t nb = __float_as_uint(nn) >> 16, lb = __float_as_uint(nl) >> 16;
             nf[w] = (nf[w] & keep) | (i ? nb << 16 : nb);
@@ -435,10 +470,10 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
       }
 #pragma unroll
       for (int hb = 0; hb < HB; ++hb) {
-        float top = fmaxf(fmaxf(x[hb][0].x, x[hb][0].y), fmaxf(x[hb][1].x, x[hb][1].y));
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-        const float mn = fmaxf(m[hb], top);
+        float tm = fmaxf(top[hb], __shfl_xor_sync(kFull, top[hb], 1));
+        tm = fmaxf(tm, __shfl_xor_sync(kFull, tm, 2));
+        if constexpr (PACK) tm = fmaxf(tm, __shfl_xor_sync(kFull, tm, 16));   // the other half tile
+        const float mn = fmaxf(m[hb], tm);
         const float al = mn == m[hb] ? 1.0f : fast_exp2(m[hb] - mn);   // 0 from -inf
         m[hb] = mn;
         l[hb] *= al;
@@ -446,7 +481,8 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           olo[hb][g] = mul2(olo[hb][g], make_float2(al, al));
-          const float r = (g & 1) ? rf[g / 2].y : rf[g / 2].x;
+          const float r = rf[g];
+          oup[hb][g] = mul2(oup[hb][g], make_float2(al * r, al * r));
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
             o[hb][g][mt][0] *= a0 * r;
@@ -461,11 +497,11 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
     for (int hb = 0; hb < HB; ++hb) {
       const float mu = m[hb] == -INFINITY ? 0.0f : m[hb];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        x[hb][j].x = fast_exp2(x[hb][j].x - mu);
-        x[hb][j].y = fast_exp2(x[hb][j].y - mu);
+      for (int jj = 0; jj < NJ; ++jj) {
+        x[hb][jj].x = fast_exp2(x[hb][jj].x - mu);
+        x[hb][jj].y = fast_exp2(x[hb][jj].y - mu);
+        l[hb] += x[hb][jj].x + x[hb][jj].y;
       }
-      l[hb] += (x[hb][0].x + x[hb][0].y) + (x[hb][1].x + x[hb][1].y);
     }
 
     // ---- P V -----------------------------------------------------------------------
@@ -484,11 +520,11 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
       }
 #pragma unroll
     for (int w = 0; w < NG / 2; ++w) {
-      uint32_t vn[2][2];
+      uint32_t vn[NJ][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int jj = 0; jj < NJ; ++jj)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) vn[j][e] = mul_bf16x2(vs[j][e][w], nf[w]);   // times 2^-R: exact
+        for (int e = 0; e < 2; ++e) vn[jj][e] = mul_bf16x2(vs[jj][e][w], nf[w]);   // times 2^-R: exact
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int g = 2 * w + i;
@@ -501,19 +537,20 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
         for (int hb = 0; hb < HB; ++hb) {
           uint32_t bh[2], bl[2];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float2 ps = mul2(x[hb][j], halves(vn[j][0], vn[j][1], i));
-            const float2 mid = fma2(halves(vs[j][0][w], vs[j][1][w], i), make_float2(8.0f, 8.0f),
-                                    halves(vl[j][0][w], vl[j][1][w], i));
-            olo[hb][g] = fma2(x[hb][j], mid, olo[hb][g]);
-            bh[j] = pack_f16(ps.x, ps.y);
-            const float2 h = unpack_f16(bh[j]);
-            if constexpr (PACK) {                    // lanes of the lo columns: what hi left over
-              const float2 r = fma2(lo_mul, h, ps);
-              bh[j] = pack_f16(r.x, r.y);
-            } else {
-              bl[j] = pack_f16(ps.x - h.x, ps.y - h.y);
-            }
+          for (int jj = 0; jj < NJ; ++jj) {
+            const float2 ps = mul2(x[hb][jj], halves(vn[jj][0], vn[jj][1], i));
+            olo[hb][g] = fma2(x[hb][jj], halves(vl[jj][0][w], vl[jj][1][w], i), olo[hb][g]);
+            oup[hb][g] = fma2(ps, make_float2(8.0f, 8.0f), oup[hb][g]);
+            bh[jj] = pack_f16(ps.x, ps.y);
+            const float2 h = unpack_f16(bh[jj]);
+            bl[jj] = pack_f16(ps.x - h.x, ps.y - h.y);
+          }
+          if constexpr (PACK) {
+            // lanes of columns 0-3 want the hi terms of both halves, those of
+            // columns 4-7 the lo terms: each keeps one of its own and is sent the other
+            const uint32_t got = __shfl_xor_sync(kFull, upper ? bh[0] : bl[0], 16);
+            bh[1] = upper ? bl[0] : got;
+            bh[0] = upper ? got : bh[0];
           }
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
@@ -533,13 +570,18 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
   // ---- leave (m, l, acc) for the merge -----------------------------------------
 #pragma unroll
   for (int hb = 0; hb < HB; ++hb) {
-    l[hb] += __shfl_xor_sync(kFull, l[hb], 1);
-    l[hb] += __shfl_xor_sync(kFull, l[hb], 2);
+    // sum over the lanes that share a head
+    auto shared = [&](float v) {
+      v += __shfl_xor_sync(kFull, v, 1);
+      v += __shfl_xor_sync(kFull, v, 2);
+      if constexpr (PACK) v += __shfl_xor_sync(kFull, v, 16);
+      return v;
+    };
+    l[hb] = shared(l[hb]);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      float z = olo[hb][g].x + olo[hb][g].y;
-      z += __shfl_xor_sync(kFull, z, 1);
-      olo[hb][g].x = z + __shfl_xor_sync(kFull, z, 2);
+      const float un = 1.0f / ((g & 1) ? bf16_hi(nf[g / 2]) : bf16_lo(nf[g / 2]));   // 2^R: exact
+      olo[hb][g].x = shared(fmaf(oup[hb][g].x + oup[hb][g].y, un, olo[hb][g].x + olo[hb][g].y));
     }
   }
   __syncthreads();                                   // ring no longer read
@@ -548,7 +590,7 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
   float *cacc = cl + kWarps4 * 16;                              // [kWarps4][GR][D]
 #pragma unroll
   for (int hb = 0; hb < HB; ++hb) {
-    if (tq == 0 && !is_lo) {
+    if (tq == 0 && !upper) {
       cm[warp * 16 + hd + 8 * hb] = m[hb];
       cl[warp * 16 + hd + 8 * hb] = l[hb];
     }
