@@ -643,6 +643,13 @@ attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
         }
       }
     };
+    // where this warp's tiles leave their logits and rows
+    [[maybe_unused]] float *mass_logit = nullptr;
+    [[maybe_unused]] uint32_t *mass_row = nullptr;
+    if constexpr (MASS) {
+      mass_logit = ws.logits + (t + warp) * (GR * kTileRows) + 4 * tq;
+      mass_row = ws.tile_row + (t + warp) * kTileRows;
+    }
     // tile q's rows: rows past the segment repeat the tile's first row (finite
     // data) and are masked out; the masks go to the warp's slot of tile q
     auto prep = [&](int q, uint32_t row, uint32_t mask) -> uint32_t {
@@ -650,10 +657,9 @@ attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
         if constexpr (MASS) {
           // columns in the order the score fragments hold them: column
           // 4 tq + 2 j + e is row 8 j + 2 tq + e
-          const long long tile = t + warp + (long long)q * kWarps;
           if (lane < kTileRows)
-            ws.tile_row[tile * kTileRows + ((lane >> 1) & 3) * 4 + (lane >> 3) * 2 + (lane & 1)] = mask ? row : kNoRow;
-          if (lane == 0) ws.tile_item[tile] = item;
+            mass_row[q * (kWarps * kTileRows) + ((lane >> 1) & 3) * 4 + (lane >> 3) * 2 + (lane & 1)] = mask ? row : kNoRow;
+          if (lane == 0) ws.tile_item[t + warp + q * kWarps] = item;
         }
         const long long gx0 = r0 + (long long)(warp + q * kWarps) * kTileRows;
         const uint32_t first = __shfl_sync(kFull, row, 0);
@@ -729,7 +735,7 @@ attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
             p[j][2 + e] = (HI && (mm & head_bit1)) ? s[j][2 + e] * sc : -INFINITY;
           }
         if constexpr (MASS) {
-          float *lg = ws.logits + ((t + warp + (long long)q * kWarps) * GR) * kTileRows + 4 * tq;
+          float *lg = mass_logit + q * (kWarps * GR * kTileRows);
           if (gq < nh) *reinterpret_cast<float4 *>(lg + gq * kTileRows) = make_float4(p[0][0], p[0][1], p[1][0], p[1][1]);
           if (HI && gq + 8 < nh)
             *reinterpret_cast<float4 *>(lg + (gq + 8) * kTileRows) = make_float4(p[0][2], p[0][3], p[1][2], p[1][3]);
@@ -784,6 +790,15 @@ attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
         split_bf16(p[0][2], p[0][3], ph[1], pl[1]);  // head gq + 8, rows 2tq, 2tq+1
         split_bf16(p[1][0], p[1][1], ph[2], pl[2]);  // head gq,     rows 8+2tq, 9+2tq
         split_bf16(p[1][2], p[1][3], ph[3], pl[3]);  // head gq + 8, rows 8+2tq, 9+2tq
+        // with accumulated weights the outputs take a third term, so that they are
+        // as exact as the weights (2.5e-7 instead of 1.4e-6 of the output)
+        [[maybe_unused]] uint32_t pr[4];
+        if constexpr (MASS) {
+          pr[0] = rest_bf16(p[0][0], p[0][1], ph[0], pl[0]);
+          pr[1] = rest_bf16(p[0][2], p[0][3], ph[1], pl[1]);
+          pr[2] = rest_bf16(p[1][0], p[1][1], ph[2], pl[2]);
+          pr[3] = rest_bf16(p[1][2], p[1][3], ph[3], pl[3]);
+        }
 #pragma unroll
         for (int nn = 0; nn < NT; nn += 2) {
           uint32_t vb[4];
@@ -793,12 +808,20 @@ attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
             mma_bf16(o[nn], pl[0], pl[1], pl[2], pl[3], vb[0], vb[1]);
             mma_bf16(o[nn + 1], ph[0], ph[1], ph[2], ph[3], vb[2], vb[3]);
             mma_bf16(o[nn + 1], pl[0], pl[1], pl[2], pl[3], vb[2], vb[3]);
+            if constexpr (MASS) {
+              mma_bf16(o[nn], pr[0], pr[1], pr[2], pr[3], vb[0], vb[1]);
+              mma_bf16(o[nn + 1], pr[0], pr[1], pr[2], pr[3], vb[2], vb[3]);
+            }
           } else {
             float u0[2] = {o[nn][0], o[nn][1]}, u1[2] = {o[nn + 1][0], o[nn + 1][1]};
             mma_bf16_top(u0, ph[0], ph[2], vb[0], vb[1], zu, zf);
             mma_bf16_top(u0, pl[0], pl[2], vb[0], vb[1], zu, zf);
             mma_bf16_top(u1, ph[0], ph[2], vb[2], vb[3], zu, zf);
             mma_bf16_top(u1, pl[0], pl[2], vb[2], vb[3], zu, zf);
+            if constexpr (MASS) {
+              mma_bf16_top(u0, pr[0], pr[2], vb[0], vb[1], zu, zf);
+              mma_bf16_top(u1, pr[0], pr[2], vb[2], vb[3], zu, zf);
+            }
             o[nn][0] = u0[0]; o[nn][1] = u0[1]; o[nn + 1][0] = u1[0]; o[nn + 1][1] = u1[1];
           }
         }

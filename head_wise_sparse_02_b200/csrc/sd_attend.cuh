@@ -117,10 +117,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(y), "f"(x));
   return r;
 }
-// p = hi + lo with hi = bf16(p), lo = bf16(p - hi): |p - hi - lo| <= 2^-17 |p|
+// p = hi + lo with hi = bf16(p), lo = bf16(p - hi): |p - hi - lo| <= 2^-16 |p|
 __device__ __forceinline__ void split_bf16(float x, float y, uint32_t &hi, uint32_t &lo) {
   hi = pack_bf16(x, y);
   lo = pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi));
+}
+
+// what hi + lo leave of p, as bf16: the three together are within 2^-24 |p|
+__device__ __forceinline__ uint32_t rest_bf16(float x, float y, uint32_t hi, uint32_t lo) {
+  return pack_bf16((x - bf16_lo(hi)) - bf16_lo(lo), (y - bf16_hi(hi)) - bf16_hi(lo));
 }
 
 // First index i in [0, n) with arr[i] >= x (n if none), arr ascending; the
@@ -288,26 +293,26 @@ __device__ __forceinline__ void merge_segment(const AttendArgs &a, const Shape &
           if (lane == 0) sden[i] += dsum;
         }
         // slots in order for every output; the loads of kBatch slots of all the
-        // thread's outputs are in flight together
-        constexpr int kBatch = OPT >= 8 ? 2 : 8;
+        // thread's outputs (channel tid % D of every (kThr / D)-th head) are in
+        // flight together
+        static_assert(kThr % D == 0, "a thread keeps its channel");
+        constexpr int kBatch = OPT >= 8 ? 2 : 8, kStep = kThr / D;
+        const int i0 = tid / D;
+        const float *pp = pbase + s0 * PS + i0 * (D + 2) + 2 + tid % D;
+        const float *fi = fw + i0 * kMergeChunk;
 #pragma unroll 1
-        for (int sl = 0; sl < nc; sl += kBatch) {
+        for (int sl = 0; sl < nc; sl += kBatch, pp += kBatch * PS, fi += kBatch) {
           float v[OPT][kBatch];
 #pragma unroll
-          for (int u = 0; u < OPT; ++u) {
-            const int x = tid + u * kThr;
-            const float *pp = pbase + (s0 + sl) * PS + (x / D) * (D + 2) + 2 + x % D;
+          for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) v[u][k] = x < nh * D && sl + k < nc ? __ldcg(pp + k * PS) : 0.0f;
-          }
+            for (int u = 0; u < OPT; ++u)
+              v[u][k] = i0 + u * kStep < nh && sl + k < nc ? __ldcg(pp + k * PS + u * (kStep * (D + 2))) : 0.0f;
 #pragma unroll
-          for (int u = 0; u < OPT; ++u) {
-            const int x = tid + u * kThr;
-            const float *fi = fw + (x < nh * D ? x / D : 0) * kMergeChunk + sl;
+          for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-              if (sl + k < nc) num[u] = fmaf(fi[k], v[u][k], num[u]);
-          }
+            for (int u = 0; u < OPT; ++u)
+              if (sl + k < nc) num[u] = fmaf(fi[u * (kStep * kMergeChunk) + k], v[u][k], num[u]);
         }
       }
       __syncthreads();
@@ -315,11 +320,8 @@ __device__ __forceinline__ void merge_segment(const AttendArgs &a, const Shape &
         ws.lse[(long long)item * kMaxGroup + tid] = make_float2(sM[tid], sden[tid] > 0.0f ? 1.0f / sden[tid] : 0.0f);
 #pragma unroll
       for (int u = 0; u < OPT; ++u) {
-        const int x = tid + u * kThr;
-        if (x < nh * D) {
-          const int i = x / D, cc = x % D;
-          a.out[((long long)b * sh.Hq + S.grp.q_head[i]) * D + cc] = sden[i] > 0.0f ? num[u] / sden[i] : 0.0f;
-        }
+        const int i = u * (kThr / D) + tid / D;
+        if (i < nh) a.out[((long long)b * sh.Hq + S.grp.q_head[i]) * D + tid % D] = sden[i] > 0.0f ? num[u] / sden[i] : 0.0f;
       }
     }
   }

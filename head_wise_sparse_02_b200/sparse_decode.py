@@ -107,7 +107,8 @@ def _check(status: int, ctx: Optional[int] = None) -> None:
         raise SparseDecodeError(status, msg)
 
 
-def _ptr(t: Optional[torch.Tensor], dtype: torch.dtype, name: str) -> Optional[int]:
+def _ptr(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, dev: Optional[int] = None) -> Optional[int]:
+    """Address of a contiguous CUDA tensor of `dtype` (on device `dev`, when given)."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
@@ -116,9 +117,18 @@ def _ptr(t: Optional[torch.Tensor], dtype: torch.dtype, name: str) -> Optional[i
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _fast(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, dev: int) -> Optional[int]:
+    """_ptr with the checks of a good argument first: a decode step's host time is mostly argument checks."""
+    if t is not None and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t, dtype, name, dev)
 
 
 def _check_sets(ctx: int, sel_idx, sel_count, batch: int) -> None:
@@ -137,10 +147,16 @@ def _check_sets(ctx: int, sel_idx, sel_count, batch: int) -> None:
         raise ValueError(f"sel_count must be [B >= {batch}, H_ret = {h_ret}], got {tuple(sel_count.shape)}")
 
 
-def _stream(stream, device=None) -> int:
+def _stream(stream, dev: Optional[int] = None) -> int:
+    """A stream's handle; None is torch's current stream of device `dev` (of the current device, without one)."""
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch.cuda.current_stream().cuda_stream if dev is None else _current_stream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+# torch's handle of the current stream without a Stream object around it, where torch has it
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 # ------------------------------------------------------------ C-named calls
@@ -366,100 +382,128 @@ def sparse_decode_mass_workspace_size(ctx: int, batch: int) -> int:
     return n.value
 
 
-def _check_tokens(slots, rows, names) -> int:
-    """Token rows are [T, Hkv, d], all of one shape, with one slot each."""
-    T = int(slots.numel())
-    for name, t in zip(names, rows):
-        if t.dim() != 3 or t.shape[0] != T or t.shape != rows[0].shape:
-            raise ValueError(f"{name} must be [T = {T}, Hkv, d] like {names[0]}, got {tuple(t.shape)}")
+def _check_tokens(slots, a, b, name_a: str, name_b: str) -> int:
+    """Token rows are [T, Hkv, d], both of one shape, with one slot each."""
+    T = slots.numel()
+    for name, t in ((name_a, a), (name_b, b)):
+        if t.dim() != 3 or t.shape[0] != T or t.shape != a.shape:
+            raise ValueError(f"{name} must be [T = {T}, Hkv, d] like {name_a}, got {tuple(t.shape)}")
     return T
 
 
 def _check_kv4(kv4_cache, heads: Optional[int], d: int) -> None:
     """The records are addressed through a raw pointer: [num_pages, Hkv, page, 5 d / 4]."""
-    if kv4_cache.dim() != 4 or kv4_cache.shape[-1] != 5 * d // 4 or (heads is not None and kv4_cache.shape[1] != heads):
-        raise ValueError(f"kv4_cache must be [num_pages, Hkv, page, 5 d / 4 = {5 * d // 4}], got "
-                         f"{tuple(kv4_cache.shape)}")
+    shape = kv4_cache.shape
+    if len(shape) != 4 or shape[3] != 5 * d // 4 or (heads is not None and shape[1] != heads):
+        raise ValueError(f"kv4_cache must be [num_pages, Hkv, page, 5 d / 4 = {5 * d // 4}], got {tuple(shape)}")
+
+
+def _check_batch(q, out, page_table, seq_lens) -> int:
+    """q and out are [B, Hq, d], page_table [>= B, MAXP], for the B lengths of seq_lens."""
+    B, shape = seq_lens.numel(), q.shape
+    if len(shape) != 3 or shape[0] != B or out.shape != shape:
+        raise ValueError(f"q and out must be [B = {B}, Hq, d], got {tuple(shape)} / {tuple(out.shape)}")
+    if page_table.dim() != 2 or page_table.shape[0] < B:
+        raise ValueError(f"page_table must be [B >= {B}, MAXP], got {tuple(page_table.shape)}")
+    return B
+
+
+def _check_mass(mass, cache) -> None:
+    """Accumulated weights lie like the caches' rows: [num_pages, Hkv, page]."""
+    if mass is not None and mass.shape != cache.shape[:3]:
+        raise ValueError(f"mass must be [num_pages, Hkv, page] = {tuple(cache.shape[:3])}, got {tuple(mass.shape)}")
 
 
 def sparse_decode_kv4_append(ctx: int, k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor,
                              kv4_cache: torch.Tensor, stream=None) -> None:
     """Write new tokens' keys and values ([T, Hkv, d] bf16) as 4-bit records."""
-    T = _check_tokens(slots, (k_new, v_new), ("k_new", "v_new"))
+    T = _check_tokens(slots, k_new, v_new, "k_new", "v_new")
     _check_kv4(kv4_cache, k_new.shape[1], k_new.shape[2])
+    dev = kv4_cache.get_device()
     _check(LIB.sparse_decode_kv4_append(
-        ctx, _ptr(k_new, torch.bfloat16, "k_new"), _ptr(v_new, torch.bfloat16, "v_new"),
-        _ptr(slots, torch.int32, "slots"), T, _ptr(kv4_cache, torch.uint8, "kv4_cache"),
-        _stream(stream, kv4_cache.device)), ctx)
+        ctx, _fast(k_new, torch.bfloat16, "k_new", dev), _fast(v_new, torch.bfloat16, "v_new", dev),
+        _fast(slots, torch.int32, "slots", dev), T, _fast(kv4_cache, torch.uint8, "kv4_cache", dev),
+        _stream(stream, dev)), ctx)
 
 
 def sparse_decode_kv4_load(ctx: int, kv4_cache: torch.Tensor, slots: torch.Tensor, k_out: torch.Tensor,
                            v_out: torch.Tensor, stream=None) -> None:
     """Read tokens back from 4-bit records as bf16 [T, Hkv, d]."""
-    T = _check_tokens(slots, (k_out, v_out), ("k_out", "v_out"))
+    T = _check_tokens(slots, k_out, v_out, "k_out", "v_out")
     _check_kv4(kv4_cache, k_out.shape[1], k_out.shape[2])
+    dev = kv4_cache.get_device()
     _check(LIB.sparse_decode_kv4_load(
-        ctx, _ptr(kv4_cache, torch.uint8, "kv4_cache"), _ptr(slots, torch.int32, "slots"), T,
-        _ptr(k_out, torch.bfloat16, "k_out"), _ptr(v_out, torch.bfloat16, "v_out"),
-        _stream(stream, kv4_cache.device)), ctx)
+        ctx, _fast(kv4_cache, torch.uint8, "kv4_cache", dev), _fast(slots, torch.int32, "slots", dev), T,
+        _fast(k_out, torch.bfloat16, "k_out", dev), _fast(v_out, torch.bfloat16, "v_out", dev),
+        _stream(stream, dev)), ctx)
 
 
 def sparse_decode_attend_kv4(ctx: int, q, kv4_cache, page_table, seq_lens, sel_idx, sel_count, out, workspace,
                              mass=None, stream=None) -> None:
     """attend on a cache of 4-bit records; with `mass`, as attend_mass."""
-    _check_sets(ctx, sel_idx, sel_count, int(seq_lens.numel()))
-    _check_kv4(kv4_cache, None, q.shape[-1])
-    stride = int(sel_idx.shape[-1]) if sel_idx is not None else 0
+    B = _check_batch(q, out, page_table, seq_lens)
+    _check_sets(ctx, sel_idx, sel_count, B)
+    _check_kv4(kv4_cache, None, q.shape[2])
+    _check_mass(mass, kv4_cache)
+    dev = q.get_device()
     _check(LIB.sparse_decode_attend_kv4(
-        ctx, _ptr(q, torch.bfloat16, "q"), _ptr(kv4_cache, torch.uint8, "kv4_cache"),
-        _ptr(page_table, torch.int32, "page_table"), _ptr(seq_lens, torch.int32, "seq_lens"),
-        int(seq_lens.numel()), _ptr(sel_idx, torch.int32, "sel_idx"), _ptr(sel_count, torch.int32, "sel_count"),
-        stride, _ptr(out, torch.float32, "out"), _ptr(mass, torch.float32, "mass"),
-        _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream(stream, q.device)), ctx)
+        ctx, _fast(q, torch.bfloat16, "q", dev), _fast(kv4_cache, torch.uint8, "kv4_cache", dev),
+        _fast(page_table, torch.int32, "page_table", dev), _fast(seq_lens, torch.int32, "seq_lens", dev), B,
+        _fast(sel_idx, torch.int32, "sel_idx", dev), _fast(sel_count, torch.int32, "sel_count", dev),
+        sel_idx.shape[-1] if sel_idx is not None else 0, _fast(out, torch.float32, "out", dev),
+        _fast(mass, torch.float32, "mass", dev), _fast(workspace, torch.uint8, "workspace", dev), workspace.numel(),
+        _stream(stream, dev)), ctx)
 
 
 def sparse_decode_select_attend_kv4(ctx: int, q_pre, q, index_cache, kv4_cache, page_table, seq_lens, sel_idx,
                                     sel_count, out, workspace, mass=None, stream=None) -> None:
     """select followed by attend_kv4 on the same sets, in one call."""
-    _check_sets(ctx, sel_idx, sel_count, int(seq_lens.numel()))
-    _check_kv4(kv4_cache, None, q.shape[-1])
-    stride = int(sel_idx.shape[-1]) if sel_idx is not None else 0
+    B = _check_batch(q, out, page_table, seq_lens)
+    _check_sets(ctx, sel_idx, sel_count, B)
+    _check_kv4(kv4_cache, None, q.shape[2])
+    _check_mass(mass, kv4_cache)
+    dev = q.get_device()
     _check(LIB.sparse_decode_select_attend_kv4(
-        ctx, _ptr(q_pre, torch.bfloat16, "q_pre"), _ptr(q, torch.bfloat16, "q"),
-        _ptr(index_cache, torch.bfloat16, "index_cache"), _ptr(kv4_cache, torch.uint8, "kv4_cache"),
-        _ptr(page_table, torch.int32, "page_table"), _ptr(seq_lens, torch.int32, "seq_lens"),
-        int(seq_lens.numel()), _ptr(sel_idx, torch.int32, "sel_idx"), _ptr(sel_count, torch.int32, "sel_count"),
-        stride, _ptr(out, torch.float32, "out"), _ptr(mass, torch.float32, "mass"),
-        _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream(stream, q.device)), ctx)
+        ctx, _fast(q_pre, torch.bfloat16, "q_pre", dev), _fast(q, torch.bfloat16, "q", dev),
+        _fast(index_cache, torch.bfloat16, "index_cache", dev), _fast(kv4_cache, torch.uint8, "kv4_cache", dev),
+        _fast(page_table, torch.int32, "page_table", dev), _fast(seq_lens, torch.int32, "seq_lens", dev), B,
+        _fast(sel_idx, torch.int32, "sel_idx", dev), _fast(sel_count, torch.int32, "sel_count", dev),
+        sel_idx.shape[-1] if sel_idx is not None else 0, _fast(out, torch.float32, "out", dev),
+        _fast(mass, torch.float32, "mass", dev), _fast(workspace, torch.uint8, "workspace", dev), workspace.numel(),
+        _stream(stream, dev)), ctx)
 
 
 def sparse_decode_attend_mass(ctx: int, q, k_cache, v_cache, page_table, seq_lens, sel_idx, sel_count, out, mass,
                               workspace, stream=None) -> None:
     """attend that adds every attention weight to mass [num_pages, Hkv, page]."""
-    _check_sets(ctx, sel_idx, sel_count, int(seq_lens.numel()))
-    stride = int(sel_idx.shape[-1]) if sel_idx is not None else 0
+    B = _check_batch(q, out, page_table, seq_lens)
+    _check_sets(ctx, sel_idx, sel_count, B)
+    _check_mass(mass, k_cache)
+    dev = q.get_device()
     _check(LIB.sparse_decode_attend_mass(
-        ctx, _ptr(q, torch.bfloat16, "q"), _ptr(k_cache, torch.bfloat16, "k_cache"),
-        _ptr(v_cache, torch.bfloat16, "v_cache"), _ptr(page_table, torch.int32, "page_table"),
-        _ptr(seq_lens, torch.int32, "seq_lens"), int(seq_lens.numel()),
-        _ptr(sel_idx, torch.int32, "sel_idx"), _ptr(sel_count, torch.int32, "sel_count"), stride,
-        _ptr(out, torch.float32, "out"), _ptr(mass, torch.float32, "mass"),
-        _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream(stream, q.device)), ctx)
+        ctx, _fast(q, torch.bfloat16, "q", dev), _fast(k_cache, torch.bfloat16, "k_cache", dev),
+        _fast(v_cache, torch.bfloat16, "v_cache", dev), _fast(page_table, torch.int32, "page_table", dev),
+        _fast(seq_lens, torch.int32, "seq_lens", dev), B, _fast(sel_idx, torch.int32, "sel_idx", dev),
+        _fast(sel_count, torch.int32, "sel_count", dev), sel_idx.shape[-1] if sel_idx is not None else 0,
+        _fast(out, torch.float32, "out", dev), _fast(mass, torch.float32, "mass", dev),
+        _fast(workspace, torch.uint8, "workspace", dev), workspace.numel(), _stream(stream, dev)), ctx)
 
 
 def sparse_decode_select_attend_mass(ctx: int, q_pre, q, index_cache, k_cache, v_cache, page_table, seq_lens, sel_idx,
                                      sel_count, out, mass, workspace, stream=None) -> None:
     """select followed by attend_mass on the same sets, in one call."""
-    _check_sets(ctx, sel_idx, sel_count, int(seq_lens.numel()))
-    stride = int(sel_idx.shape[-1]) if sel_idx is not None else 0
+    B = _check_batch(q, out, page_table, seq_lens)
+    _check_sets(ctx, sel_idx, sel_count, B)
+    _check_mass(mass, k_cache)
+    dev = q.get_device()
     _check(LIB.sparse_decode_select_attend_mass(
-        ctx, _ptr(q_pre, torch.bfloat16, "q_pre"), _ptr(q, torch.bfloat16, "q"),
-        _ptr(index_cache, torch.bfloat16, "index_cache"), _ptr(k_cache, torch.bfloat16, "k_cache"),
-        _ptr(v_cache, torch.bfloat16, "v_cache"), _ptr(page_table, torch.int32, "page_table"),
-        _ptr(seq_lens, torch.int32, "seq_lens"), int(seq_lens.numel()),
-        _ptr(sel_idx, torch.int32, "sel_idx"), _ptr(sel_count, torch.int32, "sel_count"), stride,
-        _ptr(out, torch.float32, "out"), _ptr(mass, torch.float32, "mass"),
-        _ptr(workspace, torch.uint8, "workspace"), int(workspace.numel()), _stream(stream, q.device)), ctx)
+        ctx, _fast(q_pre, torch.bfloat16, "q_pre", dev), _fast(q, torch.bfloat16, "q", dev),
+        _fast(index_cache, torch.bfloat16, "index_cache", dev), _fast(k_cache, torch.bfloat16, "k_cache", dev),
+        _fast(v_cache, torch.bfloat16, "v_cache", dev), _fast(page_table, torch.int32, "page_table", dev),
+        _fast(seq_lens, torch.int32, "seq_lens", dev), B, _fast(sel_idx, torch.int32, "sel_idx", dev),
+        _fast(sel_count, torch.int32, "sel_count", dev), sel_idx.shape[-1] if sel_idx is not None else 0,
+        _fast(out, torch.float32, "out", dev), _fast(mass, torch.float32, "mass", dev),
+        _fast(workspace, torch.uint8, "workspace", dev), workspace.numel(), _stream(stream, dev)), ctx)
 
 
 def sparse_decode_evict(ctx: int, mass, page_table, seq_lens, new_page_table, budget: int, keep_first: int,
@@ -467,27 +511,30 @@ def sparse_decode_evict(ctx: int, mass, page_table, seq_lens, new_page_table, bu
                         stream=None) -> None:
     """Shorten every sequence to `budget` tokens per KV head by accumulated
     weight, moving the kept rows of the given caches to the pages of
-    new_page_table.  kept int32 [B, Hkv, budget], new_lens int32 [B]."""
-    B = int(seq_lens.numel())
-    if kept.dim() != 3 or kept.shape[0] < B or kept.shape[1] != mass.shape[1] or kept.shape[2] != budget:
-        raise ValueError(f"kept must be [B >= {B}, Hkv = {mass.shape[1]}, budget = {budget}], got {tuple(kept.shape)}")
+    new_page_table.  kept int32 [>= B, Hkv, budget], new_lens int32 [>= B]."""
+    B, shape = seq_lens.numel(), mass.shape
+    if len(shape) != 3:
+        raise ValueError(f"mass must be [num_pages, Hkv, page], got {tuple(shape)}")
+    if kept.dim() != 3 or kept.shape[0] < B or kept.shape[1] != shape[1] or kept.shape[2] != budget:
+        raise ValueError(f"kept must be [B >= {B}, Hkv = {shape[1]}, budget = {budget}], got {tuple(kept.shape)}")
     if new_lens.numel() < B:
         raise ValueError(f"new_lens must hold {B} entries, got {new_lens.numel()}")
-    if new_page_table.dim() != 2 or new_page_table.shape[0] < B or new_page_table.shape[1] != page_table.shape[1]:
-        raise ValueError(f"new_page_table must be [B >= {B}, MAXP = {page_table.shape[1]}], got "
-                         f"{tuple(new_page_table.shape)}")
+    for name, t in (("page_table", page_table), ("new_page_table", new_page_table)):
+        if t.dim() != 2 or t.shape[0] < B or t.shape[1] != page_table.shape[1]:
+            raise ValueError(f"{name} must be [B >= {B}, MAXP = {page_table.shape[1]}], got {tuple(t.shape)}")
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("index_cache", index_cache),
                     ("kv4_cache", kv4_cache)):
-        if t is not None and tuple(t.shape[:3]) != tuple(mass.shape):
-            raise ValueError(f"{name} must be [num_pages, Hkv, page, ...] like mass {tuple(mass.shape)}, got "
+        if t is not None and t.shape[:3] != shape:
+            raise ValueError(f"{name} must be [num_pages, Hkv, page, ...] like mass {tuple(shape)}, got "
                              f"{tuple(t.shape)}")
+    dev = mass.get_device()
     _check(LIB.sparse_decode_evict(
-        ctx, _ptr(mass, torch.float32, "mass"), _ptr(page_table, torch.int32, "page_table"),
-        _ptr(seq_lens, torch.int32, "seq_lens"), B, _ptr(new_page_table, torch.int32, "new_page_table"),
-        int(budget), int(keep_first), int(keep_last), _ptr(kept, torch.int32, "kept"),
-        _ptr(new_lens, torch.int32, "new_lens"), _ptr(k_cache, torch.bfloat16, "k_cache"),
-        _ptr(v_cache, torch.bfloat16, "v_cache"), _ptr(index_cache, torch.bfloat16, "index_cache"),
-        _ptr(kv4_cache, torch.uint8, "kv4_cache"), _stream(stream, mass.device)), ctx)
+        ctx, _fast(mass, torch.float32, "mass", dev), _fast(page_table, torch.int32, "page_table", dev),
+        _fast(seq_lens, torch.int32, "seq_lens", dev), B, _fast(new_page_table, torch.int32, "new_page_table", dev),
+        budget, keep_first, keep_last, _fast(kept, torch.int32, "kept", dev),
+        _fast(new_lens, torch.int32, "new_lens", dev), _fast(k_cache, torch.bfloat16, "k_cache", dev),
+        _fast(v_cache, torch.bfloat16, "v_cache", dev), _fast(index_cache, torch.bfloat16, "index_cache", dev),
+        _fast(kv4_cache, torch.uint8, "kv4_cache", dev), _stream(stream, dev)), ctx)
 
 
 def sparse_decode_error_word(ctx: int, stream=None) -> int:
@@ -524,6 +571,11 @@ class SparseDecode:
         self.num_retrieval_heads = sparse_decode_num_retrieval_heads(self.handle)
         self.device = cfg["proj"].device
         self.max_len = cfg["max_pages_per_seq"] * cfg.get("page_size", 16)
+        # shapes that the checks of the 4-bit, weight and eviction calls compare with
+        self._rows = (cfg["num_pages"], cfg["num_kv_heads"], cfg.get("page_size", 16))
+        self._records = self._rows + (5 * cfg["head_dim"] // 4,)
+        self._heads = (cfg["num_q_heads"], cfg["head_dim"])
+        self._maxp = (cfg["max_pages_per_seq"],)
 
     def close(self):
         if self.handle:
@@ -615,89 +667,70 @@ class SparseDecode:
 
     # ---- 4-bit cache, accumulated weights and eviction
 
-    def _paged(self, t, last, name):
-        """The paged caches are addressed through raw pointers: check the whole shape."""
-        want = (self.cfg["num_pages"], self.cfg["num_kv_heads"], self.cfg.get("page_size", 16)) + last
-        if t is not None and tuple(t.shape) != want:
-            raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
+    def _own(self, shape, want, name):
+        """The paged caches, tables and rows are addressed through raw pointers by
+        the context's configuration: check the whole shape against it."""
+        if shape != want:
+            raise ValueError(f"{name} must be {want}, got {tuple(shape)}")
 
-    def _batch(self, q, page_table, seq_lens, out):
-        """q, out [B, Hq, d], page_table [B, MAXP] of a batch of seq_lens [B]."""
-        want = (int(seq_lens.numel()), self.cfg["num_q_heads"], self.cfg["head_dim"])
-        if tuple(q.shape) != want or tuple(out.shape) != want:
-            raise ValueError(f"q and out must be {want}, got {tuple(q.shape)} / {tuple(out.shape)}")
-        self._table(page_table, seq_lens, "page_table")
-
-    def _table(self, page_table, seq_lens, name):
-        if page_table.dim() != 2 or page_table.shape[0] < seq_lens.numel() or \
-                page_table.shape[1] != self.cfg["max_pages_per_seq"]:
-            raise ValueError(f"{name} must be [B >= {seq_lens.numel()}, MAXP = {self.cfg['max_pages_per_seq']}], got "
-                             f"{tuple(page_table.shape)}")
-
-    def _tokens(self, t, name):
-        if t.dim() != 3 or tuple(t.shape[1:]) != (self.cfg["num_kv_heads"], self.cfg["head_dim"]):
-            raise ValueError(f"{name} must be [T, Hkv = {self.cfg['num_kv_heads']}, d = {self.cfg['head_dim']}], got "
-                             f"{tuple(t.shape)}")
+    def _step(self, q, page_table):
+        self._own(q.shape[1:], self._heads, "q[1:]")
+        self._own(page_table.shape[1:], self._maxp, "page_table[1:]")
 
     def kv4_cache(self):
         """A zeroed cache of 4-bit records over the context's pages."""
-        shape = (self.cfg["num_pages"], self.cfg["num_kv_heads"], self.cfg.get("page_size", 16),
-                 5 * self.cfg["head_dim"] // 4)
-        return torch.zeros(shape, dtype=torch.uint8, device=self.device)
+        return torch.zeros(self._records, dtype=torch.uint8, device=self.device)
 
     def mass_cache(self):
         """Zeroed accumulated weights over the context's pages."""
-        shape = (self.cfg["num_pages"], self.cfg["num_kv_heads"], self.cfg.get("page_size", 16))
-        return torch.zeros(shape, dtype=torch.float32, device=self.device)
+        return torch.zeros(self._rows, dtype=torch.float32, device=self.device)
 
     def kv4_append(self, k_new, v_new, slots, kv4_cache, stream=None):
-        self._tokens(k_new, "k_new")
-        self._paged(kv4_cache, (5 * self.cfg["head_dim"] // 4,), "kv4_cache")
+        self._own(kv4_cache.shape, self._records, "kv4_cache")
         sparse_decode_kv4_append(self.handle, k_new, v_new, slots, kv4_cache, stream)
 
     def kv4_load(self, kv4_cache, slots, k_out, v_out, stream=None):
-        self._tokens(k_out, "k_out")
-        self._paged(kv4_cache, (5 * self.cfg["head_dim"] // 4,), "kv4_cache")
+        self._own(kv4_cache.shape, self._records, "kv4_cache")
         sparse_decode_kv4_load(self.handle, kv4_cache, slots, k_out, v_out, stream)
 
     def attend_kv4(self, q, kv4_cache, page_table, seq_lens, sel_idx, sel_count, out, workspace, mass=None,
                    stream=None):
-        self._batch(q, page_table, seq_lens, out)
-        self._paged(kv4_cache, (5 * self.cfg["head_dim"] // 4,), "kv4_cache")
-        self._paged(mass, (), "mass")
+        self._step(q, page_table)
+        self._own(kv4_cache.shape, self._records, "kv4_cache")
         sparse_decode_attend_kv4(self.handle, q, kv4_cache, page_table, seq_lens, sel_idx, sel_count, out, workspace,
                                  mass, stream)
 
     def select_attend_kv4(self, q_pre, q, index_cache, kv4_cache, page_table, seq_lens, sel_idx, sel_count, out,
                           workspace, mass=None, stream=None):
-        self._batch(q, page_table, seq_lens, out)
-        self._paged(kv4_cache, (5 * self.cfg["head_dim"] // 4,), "kv4_cache")
-        self._paged(mass, (), "mass")
+        self._step(q, page_table)
+        self._own(kv4_cache.shape, self._records, "kv4_cache")
+        self._own(index_cache.shape, self._rows + (16,), "index_cache")
         sparse_decode_select_attend_kv4(self.handle, q_pre, q, index_cache, kv4_cache, page_table, seq_lens, sel_idx,
                                         sel_count, out, workspace, mass, stream)
 
     def attend_mass(self, q, k_cache, v_cache, page_table, seq_lens, sel_idx, sel_count, out, mass, workspace,
                     stream=None):
-        self._batch(q, page_table, seq_lens, out)
-        self._paged(mass, (), "mass")
+        self._step(q, page_table)
+        self._own(mass.shape, self._rows, "mass")
         sparse_decode_attend_mass(self.handle, q, k_cache, v_cache, page_table, seq_lens, sel_idx, sel_count, out,
                                   mass, workspace, stream)
 
     def select_attend_mass(self, q_pre, q, index_cache, k_cache, v_cache, page_table, seq_lens, sel_idx, sel_count,
                            out, mass, workspace, stream=None):
-        self._batch(q, page_table, seq_lens, out)
-        self._paged(mass, (), "mass")
+        self._step(q, page_table)
+        self._own(mass.shape, self._rows, "mass")
         sparse_decode_select_attend_mass(self.handle, q_pre, q, index_cache, k_cache, v_cache, page_table, seq_lens,
                                          sel_idx, sel_count, out, mass, workspace, stream)
 
     def evict(self, mass, page_table, seq_lens, new_page_table, budget, keep_first, keep_last, kept, new_lens,
               k_cache=None, v_cache=None, index_cache=None, kv4_cache=None, stream=None):
-        d = self.cfg["head_dim"]
-        self._paged(mass, (), "mass")
-        self._table(page_table, seq_lens, "page_table")
+        d = self._heads[1]
+        self._own(mass.shape, self._rows, "mass")
+        self._own(page_table.shape[1:], self._maxp, "page_table[1:]")
         for name, t, last in (("k_cache", k_cache, d), ("v_cache", v_cache, d), ("index_cache", index_cache, 16),
                               ("kv4_cache", kv4_cache, 5 * d // 4)):
-            self._paged(t, (last,), name)
+            if t is not None:
+                self._own(t.shape[3:], (last,), name + "[3:]")
         sparse_decode_evict(self.handle, mass, page_table, seq_lens, new_page_table, budget, keep_first, keep_last,
                             kept, new_lens, k_cache, v_cache, index_cache, kv4_cache, stream)
 
