@@ -45,7 +45,7 @@ constexpr int kMinSlice = 2048;         // positions per CTA below which a clust
 constexpr int kBins = 2048;             // 11 bits a pass
 constexpr size_t kKeepKeysMax = 128 * 1024;   // bytes of keys held in shared memory, at most
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;
-constexpr uint32_t kZeroKey = 0x80000000u;    // order_key(0)
+constexpr uint32_t kZeroKey = 0x80000000u;    // weight_key(0)
 constexpr int kMoveThreads = 256;
 constexpr int kMoveBatch = 4;           // loads in flight per thread
 constexpr int kMoveMany = 1 << 16;      // rows from which a move CTA takes 128 instead of 32
@@ -53,6 +53,16 @@ constexpr int kMoveMany = 1 << 16;      // rows from which a move CTA takes 128 
 __device__ __forceinline__ long long clamped_len(const EvictArgs &a, const Shape &sh, int b) {
   const long long N = a.seq_lens[b];
   return N < 0 ? 0 : std::min<long long>(N, sh.max_len);
+}
+
+// Order-preserving key of a weight's bits (-0 as +0; a NaN by its sign: above
+// every number or below), and back
+__device__ __forceinline__ uint32_t weight_key(float f) {
+  const uint32_t u = __float_as_uint(f) == 0x80000000u ? 0u : __float_as_uint(f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_weight(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
 struct KeepShared {
@@ -92,7 +102,7 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
     const int page = __ldg(pt + j / kPage);
     if (page < 0 || page >= sh.num_pages) return make_uint4(0u, 0u, 0u, 0u);   // reported by the move
     const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.mass + ((long long)page * sh.Hkv + g) * kPage + j % kPage));
-    return make_uint4(order_key(v.x), order_key(v.y), order_key(v.z), order_key(v.w));
+    return make_uint4(weight_key(v.x), weight_key(v.y), weight_key(v.z), weight_key(v.w));
   };
   uint4 *keys4 = reinterpret_cast<uint4 *>(dyn + kBins / C);
   auto keys_at = [&](int j) -> uint4 { return KEYS ? keys4[(j - j0) / 4] : load4(j); };
@@ -278,8 +288,8 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       if (at[u] >= 0) kept[at[u]] = j + 4 * lane + u;
-      if (k[u] != 0u && page[u] >= 0 && page[u] < sh.num_pages)    // bad pages are reported by the move
-        a.mass[((long long)page[u] * sh.Hkv + g) * kPage + at[u] % kPage] = key_to_float(k[u]);
+      if (page[u] >= 0 && page[u] < sh.num_pages)                  // bad pages are reported by the move
+        a.mass[((long long)page[u] * sh.Hkv + g) * kPage + at[u] % kPage] = key_weight(k[u]);
     }
     const uint32_t tot = __shfl_sync(kFull, incl, 31);
     gt += tot & 0xFFFFu;

@@ -39,6 +39,8 @@ class DecodeStep:
             (num_pages, Hkv, page, 16), dtype=torch.bfloat16, device=dev)
         self.workspace, self.sel_idx, self.sel_count = self.sd.alloc(self.batch)
         self.out = torch.empty((self.batch, num_q_heads, d), dtype=torch.float32, device=dev)
+        self.kv4: Optional[torch.Tensor] = None                         # 4-bit records (make_kv4)
+        self.mass: Optional[torch.Tensor] = None                        # accumulated weights (keep_mass)
 
     def build_index(self, slots: torch.Tensor, keys: torch.Tensor, stream=None):
         """index_keys over the given slots (e.g. every cached position at setup)."""
@@ -117,6 +119,79 @@ class DecodeStep:
                                     self.local_v, self.page_table, self.seq_lens, self.sel_idx, self.sel_count,
                                     self.out, self.workspace, stream)
         return self.out
+
+    # ---- 4-bit cache, accumulated weights, eviction
+
+    def _positions(self):
+        """Sequence, position and slot of every cached token."""
+        dev = self.k_cache.device
+        lens = self.seq_lens.tolist()
+        seq = torch.cat([torch.full((n,), b, dtype=torch.long, device=dev) for b, n in enumerate(lens)] +
+                        [torch.zeros(0, dtype=torch.long, device=dev)])
+        pos = torch.cat([torch.arange(n, device=dev) for n in lens] + [torch.zeros(0, dtype=torch.long, device=dev)])
+        return seq, pos, self.page_table[seq, pos // 16].long() * 16 + pos % 16
+
+    def make_kv4(self, stream=None):
+        """Build the cache of 4-bit records from the full caches (every cached token)."""
+        self.kv4 = self.sd.kv4_cache()
+        _, _, slot = self._positions()
+        for at in range(0, slot.numel(), 1 << 16):                      # bounded copies of the rows
+            s = slot[at:at + (1 << 16)]
+            k = self.k_cache[s // 16, :, s % 16].contiguous()
+            v = self.v_cache[s // 16, :, s % 16].contiguous()
+            self.sd.kv4_append(k, v, s.to(torch.int32), self.kv4, stream)
+
+    def keep_mass(self):
+        """Accumulate the attention weights from here on (and size the workspace for it)."""
+        self.mass = self.sd.mass_cache()
+        self.workspace = self.sd.alloc(self.batch, mass=True)[0]
+
+    def attend_kv4(self, q: torch.Tensor, sel_idx=None, sel_count=None, stream=None) -> torch.Tensor:
+        """attend on the 4-bit cache (adding to the accumulated weights, if kept)."""
+        self.sd.attend_kv4(q, self.kv4, self.page_table, self.seq_lens,
+                           self.sel_idx if sel_idx is None else sel_idx,
+                           self.sel_count if sel_count is None else sel_count, self.out, self.workspace, self.mass,
+                           stream)
+        return self.out
+
+    def select_attend_kv4(self, q_pre: torch.Tensor, q: torch.Tensor, stream=None) -> torch.Tensor:
+        """select then attend_kv4 on the same sets, joined in one call."""
+        self.sd.select_attend_kv4(q_pre, q, self.index_cache, self.kv4, self.page_table, self.seq_lens, self.sel_idx,
+                                  self.sel_count, self.out, self.workspace, self.mass, stream)
+        return self.out
+
+    def select_attend_mass(self, q_pre: torch.Tensor, q: torch.Tensor, stream=None) -> torch.Tensor:
+        """select_attend that adds to the accumulated weights."""
+        self.sd.select_attend_mass(q_pre, q, self.index_cache, self.k_cache, self.v_cache, self.page_table,
+                                   self.seq_lens, self.sel_idx, self.sel_count, self.out, self.mass, self.workspace,
+                                   stream)
+        return self.out
+
+    def step_kv4(self, q_pre: torch.Tensor, q: torch.Tensor, new_k_pre: torch.Tensor, new_k: torch.Tensor,
+                 new_v: torch.Tensor, new_slots: torch.Tensor, stream=None) -> torch.Tensor:
+        """One decode step on the 4-bit cache: append and index the new tokens, then
+        select and attend."""
+        self.sd.kv4_append(new_k, new_v, new_slots, self.kv4, stream)
+        self.sd.index_keys(new_k_pre, new_slots, self.index_cache, stream)
+        return self.select_attend_kv4(q_pre, q, stream)
+
+    def evict(self, new_page_table: torch.Tensor, budget: int, keep_first: Optional[int] = None,
+              keep_last: Optional[int] = None, stream=None) -> torch.Tensor:
+        """Shorten every sequence to at most `budget` tokens per KV head by accumulated
+        weight and continue on the new pages; the sinks and the window stay by
+        default.  Returns the kept positions [B, Hkv, budget] (entries past a
+        sequence's new length are -1)."""
+        cfg = self.sd.cfg
+        first = cfg.get("num_sinks", 0) if keep_first is None else keep_first
+        last = cfg.get("window", 0) if keep_last is None else keep_last
+        kept = torch.full((self.batch, self.k_cache.shape[1], budget), -1, dtype=torch.int32,
+                          device=self.k_cache.device)
+        lens = torch.empty_like(self.seq_lens)
+        caches = dict(kv4_cache=self.kv4) if self.kv4 is not None else dict(k_cache=self.k_cache, v_cache=self.v_cache)
+        self.sd.evict(self.mass, self.page_table, self.seq_lens, new_page_table, budget, first, last, kept, lens,
+                      index_cache=self.index_cache, stream=stream, **caches)
+        self.page_table, self.seq_lens = new_page_table, lens
+        return kept
 
     def error_word(self, stream=None) -> int:
         return self.sd.error_word(stream)

@@ -126,7 +126,7 @@ def _ptr(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, dev: Optional
 
 def _fast(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, dev: int) -> Optional[int]:
     """_ptr with the checks of a good argument first: a decode step's host time is mostly argument checks."""
-    if t is not None and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+    if t is not None and dev >= 0 and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
     return _ptr(t, dtype, name, dev)
 

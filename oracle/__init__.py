@@ -9,3 +9,4 @@ imports it.
 from .sparse_decode_oracle import *  # noqa: F401,F403
 from .head_classifier_oracle import *  # noqa: F401,F403
 from .prefill_oracle import *  # noqa: F401,F403
+from .kv_memory_oracle import *  # noqa: F401,F403
