@@ -162,14 +162,17 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
         S.share = n;
       }
       cl.sync();                                                 // every histogram read, every share summed
-      // the share that holds the need-th count from the top, then its bin
-      uint32_t before = 0u;
-      int owner = 0;
-      for (; owner < C - 1; ++owner) {
-        const uint32_t n = *cl.map_shared_rank(&S.share, owner);
-        if (before + n >= (uint32_t)need) break;
-        before += n;
+      // the share that holds the need-th count from the top, then its bin (lane r
+      // reads share r, so that the remote reads are one latency)
+      const uint32_t mine_r = lane < C ? *cl.map_shared_rank(&S.share, lane) : 0u;
+      uint32_t upto = mine_r;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(kFull, upto, o);
+        if (lane >= o) upto += y;
       }
+      const int owner = __ffs(__ballot_sync(kFull, upto >= (uint32_t)need)) - 1;   // below C: the shares hold need
+      const uint32_t before = __shfl_sync(kFull, upto - mine_r, owner);
       const uint32_t *sum = cl.map_shared_rank(sums, owner);
       uint32_t mine[kBins / kKeepThreads];
       tot = 0u;
@@ -251,18 +254,24 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
     S.eq = y;
   }
   cl.sync();
-  uint32_t gt = 0u, eq = 0u;                                     // before this warp's run
-  for (int r = 0; r < rank; ++r) {
-    gt += *cl.map_shared_rank(&S.gt, r);
-    eq += *cl.map_shared_rank(&S.eq, r);
-  }
+  uint32_t gt = lane < rank ? *cl.map_shared_rank(&S.gt, lane) : 0u;   // before this warp's run
+  uint32_t eq = lane < rank ? *cl.map_shared_rank(&S.eq, lane) : 0u;
+  gt = __reduce_add_sync(kFull, gt);
+  eq = __reduce_add_sync(kFull, eq);
   for (int w = 0; w < warp; ++w) {
     gt += S.wgt[w];
     eq += S.weq[w];
   }
   cg::cluster_group::arrival_token token = cl.barrier_arrive();  // this CTA has read the others' counts
   int32_t *kept = a.kept + ((long long)b * sh.Hkv + g) * a.budget;
-  const int32_t *npt = a.new_page_table + (long long)b * sh.max_pages;
+  // new pages of the slots this warp can write in a run of 1024 positions, two per lane and one more
+  const int page0 = (int)(gt + std::min(eq, (uint32_t)need)) / kPage;
+  auto new_page = [&](int p) {
+    return p < sh.max_pages ? __ldg(a.new_page_table + (long long)b * sh.max_pages + p) : -1;
+  };
+  const bool paged = run <= 32 * 2 * kPage;          // else every slot looks its page up
+  const int npage0 = paged ? new_page(page0 + lane) : -1, npage1 = paged ? new_page(page0 + 32 + lane) : -1;
+  const int npage2 = paged ? new_page(page0 + 64) : -1;
   for (int j = w0; j < w1; j += 128) {
     uint32_t bits;
     uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
@@ -281,7 +290,13 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
     for (int u = 0; u < 4; ++u) {
       const bool one = bits & (1u << u), tie = bits & (16u << u);
       at[u] = one || (tie && e1 < (uint32_t)need) ? (int)(g1 + std::min(e1, (uint32_t)need)) : -1;
-      page[u] = at[u] >= 0 ? __ldg(npt + at[u] / kPage) : -1;
+      if (paged) {
+        const int o = at[u] >= 0 ? at[u] / kPage - page0 : 0;
+        const int lo = __shfl_sync(kFull, npage0, o & 31), hi = __shfl_sync(kFull, npage1, o & 31);
+        page[u] = at[u] < 0 ? -1 : o < 32 ? lo : o < 64 ? hi : npage2;
+      } else {
+        page[u] = at[u] >= 0 ? new_page(at[u] / kPage) : -1;
+      }
       g1 += one;
       e1 += tie;
     }
