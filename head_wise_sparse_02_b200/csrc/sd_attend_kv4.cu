@@ -33,11 +33,11 @@
 //        in the layout that P V wants for B;
 //   P V  channels on M (A = value codes), heads on N.
 // Column n of S is row (n >> 1) + 4 (n & 1) of its half tile, which spreads the
-// value loads over the banks.  With at most four heads nothing is done twice for
-// the unused rows and columns: rows 0-3 of S take the first half tile and rows
-// 4-7 the second (two products into one accumulator, each with zeros for the
-// other's queries), so a lane scales and weighs two rows instead of four, and
-// columns 0-3 of P V carry the hi terms and 4-7 the lo terms, half the products.
+// value loads over the banks.  With at most four heads the unused rows and
+// columns do the other half of the work: rows 4-7 of S repeat the heads, so that
+// their lanes take the second half tile's scores and every lane scales and weighs
+// two rows instead of four, and columns 0-3 of P V carry the hi terms and 4-7 the
+// lo terms, half the products.
 #include "sd_attend.cuh"
 
 namespace sd {
@@ -212,10 +212,7 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
   // ---- queries: A fragments (heads on M; k = the channels of the record's
   // words: lane tq holds channels 8 tq .. 8 tq + 7 of every group, nibble pairs
   // (i, i + 4)), and the sums over the groups' channels; all times 2^k
-  // With at most four heads [.][0] and [.][1] are the queries of rows 0-3 and of
-  // rows 4-7, zero in the others.
-  constexpr int QB = PACK ? 2 : HB;
-  uint32_t qa[NG][2][QB][2];
+  uint32_t qa[NG][2][HB][2];
   float qs[HB][NG], qsc[HB];
 #pragma unroll
   for (int hb = 0; hb < HB; ++hb) {
@@ -248,14 +245,6 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
       sum += __shfl_xor_sync(kFull, sum, 1);
       sum += __shfl_xor_sync(kFull, sum, 2);
       qs[hb][g] = sum * f;
-      if constexpr (PACK)
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            qa[g][ks][1][i] = upper ? qa[g][ks][0][i] : 0u;
-            qa[g][ks][0][i] = upper ? 0u : qa[g][ks][0][i];
-          }
     }
   }
   float m[HB], l[HB], o[HB][NG][2][4];
@@ -383,11 +372,17 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
         for (int u = 0; u < (PACK ? 2 : 1); ++u) {
           const uint32_t w = kw[PACK ? u : jj][g], w8 = w >> 8;
           const uint32_t b0 = low_codes(w), b1 = high_codes(w), b2 = low_codes(w8), b3 = high_codes(w8);
-          const uint32_t a1 = HB == 2 ? qa[g][0][QB - 1][0] : 0u, a3 = HB == 2 ? qa[g][0][QB - 1][1] : 0u;
-          const uint32_t c1 = HB == 2 ? qa[g][1][QB - 1][0] : 0u, c3 = HB == 2 ? qa[g][1][QB - 1][1] : 0u;
-          if (u == 0) mma_f16_first(s, qa[g][0][u][0], a1, qa[g][0][u][1], a3, b0, b1);
-          else mma_f16(s, qa[g][0][u][0], a1, qa[g][0][u][1], a3, b0, b1);
-          mma_f16(s, qa[g][1][u][0], c1, qa[g][1][u][1], c3, b2, b3);
+          const uint32_t a1 = HB == 2 ? qa[g][0][HB - 1][0] : 0u, a3 = HB == 2 ? qa[g][0][HB - 1][1] : 0u;
+          const uint32_t c1 = HB == 2 ? qa[g][1][HB - 1][0] : 0u, c3 = HB == 2 ? qa[g][1][HB - 1][1] : 0u;
+          float t[4];
+          mma_f16_first(t, qa[g][0][0][0], a1, qa[g][0][0][1], a3, b0, b1);
+          mma_f16(t, qa[g][1][0][0], c1, qa[g][1][0][1], c3, b2, b3);
+          if (u == 0) {
+            s[0] = t[0]; s[1] = t[1]; s[2] = t[2]; s[3] = t[3];
+          } else {
+            s[0] = upper ? t[0] : s[0];
+            s[1] = upper ? t[1] : s[1];
+          }
         }
         // codes were about 8: 8 times the channels' sum joins here
         const float2 sg = halves(mk[0][g / 2], mk[1][g / 2], g & 1);
