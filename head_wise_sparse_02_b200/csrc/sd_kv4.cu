@@ -48,16 +48,34 @@ struct Place {
 
 // slot -> record, or -1 (with the error bit) when the slot is outside the pool
 __device__ __forceinline__ long long record_of(int slot, int head, const Shape &sh, unsigned *err, bool report) {
-  if (slot < 0 || slot / kPage >= sh.num_pages) {
+  const uint32_t page = (uint32_t)slot / kPage;                                // of a negative slot: past any pool
+  if (page >= (uint32_t)sh.num_pages || slot < 0) {
     if (report) raise_error(err, SD_EBIT_SLOT);
     return -1;
   }
-  return ((uint32_t)(slot / kPage) * sh.Hkv + head) * kPage + slot % kPage;   // below 2^32 by init's check
+  return (page * (uint32_t)sh.Hkv + head) * kPage + (uint32_t)slot % kPage;   // below 2^32 by init's check
 }
 
 __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {   // NaN if either is
   uint32_t r;
   asm("min.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// two float32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{.reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};"
+      " fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d;}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
 
@@ -86,13 +104,17 @@ __device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[4], float lo, f
   asm("rcp.approx.f32 %0, %1;\n" : "=f"(inv) : "f"(s));
   constexpr float kRint = 12582912.0f;               // 1.5 * 2^23: adding and taking it off rounds to nearest even
   const float half = 0.5f * s;
-  float off = 0.0f, q[8];
+  const float2 nlo = make_float2(-lo, -lo), inv2 = make_float2(inv, inv), ns = make_float2(-s, -s);
+  float off = 0.0f;
+  float2 q2[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float d = (i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2])) - lo;
-    q[i] = fmaf(d, inv, kRint) - kRint;
-    off = fmaxf(off, fabsf(fmaf(-q[i], s, d)));
+  for (int i = 0; i < 4; ++i) {
+    const float2 d = add2(make_float2(bf16_lo(w[i]), bf16_hi(w[i])), nlo);
+    q2[i] = add2(fma2(d, inv2, make_float2(kRint, kRint)), make_float2(-kRint, -kRint));
+    const float2 e = fma2(q2[i], ns, d);
+    asm("max.abs.f32 %0, %0, %1, %2;\n" : "+f"(off) : "f"(e.x), "f"(e.y));
   }
+  float q[8] = {q2[0].x, q2[0].y, q2[1].x, q2[1].y, q2[2].x, q2[2].y, q2[3].x, q2[3].y};
   const bool tiny = s < 1e-30f;
   if (off > 0.9999f * half || tiny) {
 #pragma unroll

@@ -574,6 +574,10 @@ class SparseDecode:
         # shapes that the checks of the 4-bit, weight and eviction calls compare with
         self._rows = (cfg["num_pages"], cfg["num_kv_heads"], cfg.get("page_size", 16))
         self._records = self._rows + (5 * cfg["head_dim"] // 4,)
+        self._kv_rows = self._rows + (cfg["head_dim"],)
+        self._index_rows = self._rows + (cfg.get("index_dim", 16),)
+        self._kv_row = (cfg["num_kv_heads"], cfg["head_dim"])
+        self._dev = self.device.index if self.device.index is not None else torch.cuda.current_device()
         self._heads = (cfg["num_q_heads"], cfg["head_dim"])
         self._maxp = (cfg["max_pages_per_seq"],)
 
@@ -686,12 +690,30 @@ class SparseDecode:
         return torch.zeros(self._rows, dtype=torch.float32, device=self.device)
 
     def kv4_append(self, k_new, v_new, slots, kv4_cache, stream=None):
-        self._own(kv4_cache.shape, self._records, "kv4_cache")
-        sparse_decode_kv4_append(self.handle, k_new, v_new, slots, kv4_cache, stream)
+        T = slots.numel()
+        rows = (T,) + self._kv_row
+        if k_new.shape != rows or v_new.shape != rows or kv4_cache.shape != self._records:
+            self._own(k_new.shape, rows, "k_new")
+            self._own(v_new.shape, rows, "v_new")
+            self._own(kv4_cache.shape, self._records, "kv4_cache")
+        dev = self._dev
+        _check(LIB.sparse_decode_kv4_append(
+            self.handle, _fast(k_new, torch.bfloat16, "k_new", dev), _fast(v_new, torch.bfloat16, "v_new", dev),
+            _fast(slots, torch.int32, "slots", dev), T, _fast(kv4_cache, torch.uint8, "kv4_cache", dev),
+            _stream(stream, dev)), self.handle)
 
     def kv4_load(self, kv4_cache, slots, k_out, v_out, stream=None):
-        self._own(kv4_cache.shape, self._records, "kv4_cache")
-        sparse_decode_kv4_load(self.handle, kv4_cache, slots, k_out, v_out, stream)
+        T = slots.numel()
+        rows = (T,) + self._kv_row
+        if k_out.shape != rows or v_out.shape != rows or kv4_cache.shape != self._records:
+            self._own(k_out.shape, rows, "k_out")
+            self._own(v_out.shape, rows, "v_out")
+            self._own(kv4_cache.shape, self._records, "kv4_cache")
+        dev = self._dev
+        _check(LIB.sparse_decode_kv4_load(
+            self.handle, _fast(kv4_cache, torch.uint8, "kv4_cache", dev), _fast(slots, torch.int32, "slots", dev), T,
+            _fast(k_out, torch.bfloat16, "k_out", dev), _fast(v_out, torch.bfloat16, "v_out", dev),
+            _stream(stream, dev)), self.handle)
 
     def attend_kv4(self, q, kv4_cache, page_table, seq_lens, sel_idx, sel_count, out, workspace, mass=None,
                    stream=None):
@@ -704,7 +726,7 @@ class SparseDecode:
                           workspace, mass=None, stream=None):
         self._step(q, page_table)
         self._own(kv4_cache.shape, self._records, "kv4_cache")
-        self._own(index_cache.shape, self._rows + (16,), "index_cache")
+        self._own(index_cache.shape, self._index_rows, "index_cache")
         sparse_decode_select_attend_kv4(self.handle, q_pre, q, index_cache, kv4_cache, page_table, seq_lens, sel_idx,
                                         sel_count, out, workspace, mass, stream)
 
@@ -724,13 +746,12 @@ class SparseDecode:
 
     def evict(self, mass, page_table, seq_lens, new_page_table, budget, keep_first, keep_last, kept, new_lens,
               k_cache=None, v_cache=None, index_cache=None, kv4_cache=None, stream=None):
-        d = self._heads[1]
         self._own(mass.shape, self._rows, "mass")
         self._own(page_table.shape[1:], self._maxp, "page_table[1:]")
-        for name, t, last in (("k_cache", k_cache, d), ("v_cache", v_cache, d), ("index_cache", index_cache, 16),
-                              ("kv4_cache", kv4_cache, 5 * d // 4)):
-            if t is not None:
-                self._own(t.shape[3:], (last,), name + "[3:]")
+        for t, want, name in ((k_cache, self._kv_rows, "k_cache"), (v_cache, self._kv_rows, "v_cache"),
+                              (index_cache, self._index_rows, "index_cache"), (kv4_cache, self._records, "kv4_cache")):
+            if t is not None and t.shape != want:
+                self._own(t.shape, want, name)
         sparse_decode_evict(self.handle, mass, page_table, seq_lens, new_page_table, budget, keep_first, keep_last,
                             kept, new_lens, k_cache, v_cache, index_cache, kv4_cache, stream)
 
