@@ -126,9 +126,7 @@ constexpr int kMinSegTiles = 8;         // tiles a CTA takes at least (two per w
 
 template <typename T>
 __device__ __forceinline__ T tiles_per_segment(T W, int ni, int grid) {
-  const int waves = (2 * ni + grid - 1) / grid;
-  int slots = grid * (waves > 1 ? waves : 1);
-  if (slots > kMaxSegments) slots = kMaxSegments;
+  const int slots = segment_slots(grid, ni);
   const T room = slots > ni ? slots - ni : 1;
   const T per = (W + room - 1) / room;
   return per > kMinSegTiles ? per : T(kMinSegTiles);
@@ -485,18 +483,36 @@ attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
   pdl_trigger();
 
   // ---- this CTA's share of the tiles -----------------------------------------
-  const long long W = __ldcg(ws.tstart + ap.ni);
-  // with fewer tiles than CTAs only the first W take part (one tile each), so
-  // every CTA between an item's first and last one holds some of its tiles
-  const long long P = std::min<long long>(gridDim.x, W), c = blockIdx.x;
-  if (c >= P) return;
-  const long long t0 = W * c / P, t1 = W * (c + 1) / P;
-  // CTA holding tile x: the largest c' with floor(W c' / P) <= x
-  auto cta_of = [&](long long x) { return ((x + 1) * P - 1) / W; };
-  if (warp == 0) {
-    const int i = warp_lower_bound<long long>(ws.tstart, ap.ni + 1, t0 + 1, lane) - 1;   // tstart[i] <= t0 < tstart[i+1]
-    if (lane == 0) S.item = i;
+  // [t0, t1) of all tiles of all items; with MASS a share of one item, as the
+  // layout wrote it (no search at the start, no second item: 80 -> 72 us at B 8,
+  // 128K, 2%, with the weights pass)
+  [[maybe_unused]] Segment seg{};
+  [[maybe_unused]] long long W = 0, P = 0;
+  const long long c = blockIdx.x;
+  long long t0, t1;
+  if constexpr (MASS) {
+    const int n_seg = __ldcg(ws.n_seg);
+    const int4 s0 = __ldcg(reinterpret_cast<const int4 *>(ws.seg + c));
+    const int4 s1 = __ldcg(reinterpret_cast<const int4 *>(ws.seg + c) + 1);
+    if (c >= n_seg) return;
+    seg = Segment{s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, ((long long)s1.w << 32) | (uint32_t)s1.z};
+    t0 = seg.tile;
+    t1 = t0 + seg.tiles;
+  } else {
+    W = __ldcg(ws.tstart + ap.ni);
+    // with fewer tiles than CTAs only the first W take part (one tile each), so
+    // every CTA between an item's first and last one holds some of its tiles
+    P = std::min<long long>(gridDim.x, W);
+    if (c >= P) return;
+    t0 = W * c / P;
+    t1 = W * (c + 1) / P;
+    if (warp == 0) {
+      const int i = warp_lower_bound<long long>(ws.tstart, ap.ni + 1, t0 + 1, lane) - 1;   // tstart[i] <= t0 < tstart[i+1]
+      if (lane == 0) S.item = i;
+    }
   }
+  // CTA holding tile x: the largest c' with floor(W c' / P) <= x
+  [[maybe_unused]] auto cta_of = [&](long long x) { return ((x + 1) * P - 1) / W; };
 
   // cp.async mapping: a tile's K rows and its V rows are copied separately
   // (one commit group each), whole rows per instruction (coalesced): lanes
@@ -521,12 +537,21 @@ attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
   long long t = t0;
   while (t < t1) {
     __syncthreads();                                   // S.item set; the previous item's smem no longer read
-    int item = S.item;
-    long long ts = __ldcg(ws.tstart + item), te = __ldcg(ws.tstart + item + 1);
-    while (te <= t) {                                  // skip items without tiles
-      ++item;
-      ts = te;
+    int item;
+    long long ts, te;                                  // tiles of the item (of the share, with MASS: te)
+    if constexpr (MASS) {
+      item = seg.item;
+      ts = seg.tile - seg.tile0;
+      te = t1;
+    } else {
+      item = S.item;
+      ts = __ldcg(ws.tstart + item);
       te = __ldcg(ws.tstart + item + 1);
+      while (te <= t) {                                // skip items without tiles
+        ++item;
+        ts = te;
+        te = __ldcg(ws.tstart + item + 1);
+      }
     }
     const long long seg_end = std::min(t1, te);
     int b;
@@ -534,10 +559,10 @@ attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
     const Group &grp_g = item_group(tb, ap, item, b, is_ret);
     if (tid == 0) S.grp = grp_g;
     const long long N = clamp_len(a, sh, b);
-    const long long T = __ldcg(ws.item_rows + item);
+    const long long T = MASS ? seg.rows : __ldcg(ws.item_rows + item);
     const long long r0 = (t - ts) * kTileRows;
     const long long r1 = std::min(T, (seg_end - ts) * kTileRows);
-    const long long first = cta_of(ts), last = cta_of(te - 1);
+    const long long first = MASS ? seg.first : cta_of(ts), last = MASS ? seg.last : cta_of(te - 1);
     const int gi = is_ret ? item % tb.n_ret : 0;
     const long long slot0 = ((long long)b * tb.n_ret + gi) * ap.ns;
     const int ns_item = is_ret ? (int)((N + ap.span - 1) / ap.span) : 0;
@@ -843,7 +868,8 @@ attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
         cacc[(warp * GR + gq + 8) * D + cc + 1] = o[nn][3];
       }
     }
-    merge_segment<D, GR, MASS, kWarps>(a, sh, ws, S, dyn, GR, c + item, item, first, last, first + item, b, nh);
+    merge_segment<D, GR, MASS, kWarps>(a, sh, ws, S, dyn, GR, MASS ? c : c + item, item, first, last,
+                                       MASS ? first : first + item, b, nh);
     t = seg_end;
     if (tid == 0) S.item = item + 1;
   }
@@ -903,19 +929,18 @@ AttLayout att_layout(const Shape &sh, const Tables &tb, int batch, long long loc
   return L;
 }
 
+// Shared memory of the main kernel and its CTAs that fit the device at once
 template <int D, int GR, bool MASS>
-cudaError_t launch_main(const AttendArgs &a, const Shape &sh, const Tables &tb, const AttParams &p, const AttWs &ws,
-                        cudaStream_t st) {
+cudaError_t config_main(const AttParams &p, size_t *bytes, int *grid) {
   const size_t ring = (size_t)kWarps * kTileRing * (2 * kTileRows * (2 * D + 16));
   const size_t lists = (size_t)kWarps * kTileRing * kTileRows * 2 + (size_t)(p.ns + 1) * 4;
   const size_t merge = std::max((size_t)kWarps * 32 * 4 + (size_t)kWarps * GR * D * 4,
                                 (size_t)GR * (kMergeChunk + 2) * 4);
-  const size_t bytes = std::max(ring + lists, merge);
-  const cudaError_t e = set_smem(attend_main_kernel<D, GR, MASS>, bytes);
+  *bytes = std::max(ring + lists, merge);
+  const cudaError_t e = set_smem(attend_main_kernel<D, GR, MASS>, *bytes);
   if (e != cudaSuccess) return e;
-  const int grid = resident_ctas(attend_main_kernel<D, GR, MASS>, kThreads, bytes);
-  if (grid <= 0) return cudaErrorInvalidConfiguration;
-  return launch_pdl(attend_main_kernel<D, GR, MASS>, dim3(grid), dim3(kThreads), bytes, st, 0, a, sh, tb, p, ws);
+  *grid = resident_ctas(attend_main_kernel<D, GR, MASS>, kThreads, *bytes);
+  return *grid > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
 template <int D, int GR>
@@ -931,15 +956,26 @@ cudaError_t launch_t(const AttendArgs &a, const Shape &sh, const Tables &tb, con
     e = launch_pdl(attend_plan_kernel<D, GR>, grid, dim3(kPlanThreads), pbytes, st, 0, a, sh, tb, p, ws, only);
     if (e != cudaSuccess) return e;
   }
-  const int seg_grid = a.kv4 ? kv4_main_grid(sh, tb, p, GR, a.mass != nullptr) : 0;
-  if (a.kv4 && seg_grid <= 0) return cudaErrorInvalidConfiguration;
+  size_t bytes = 0;
+  int grid = 0;                                        // CTAs that take the items' shares, or all tiles' (bf16 alone)
+  if (a.kv4) {
+    grid = kv4_main_grid(sh, tb, p, GR, a.mass != nullptr);
+    if (grid <= 0) return cudaErrorInvalidConfiguration;
+  } else {
+    e = a.mass ? config_main<D, GR, true>(p, &bytes, &grid) : config_main<D, GR, false>(p, &bytes, &grid);
+    if (e != cudaSuccess) return e;
+  }
+  const int seg_grid = a.kv4 || a.mass ? std::min(grid, kMaxSegments) : 0;
   e = launch_pdl(attend_prefix_kernel<D>, dim3(1), dim3(std::min(1024, std::max(128, pow2_ceil(p.ni)))), 0, st, 0, a, sh, tb, p, ws,
                  seg_grid);
   if (e != cudaSuccess) return e;
   if (a.kv4)
     e = launch_attend_kv4_main(a, sh, tb, p, ws, GR, st);
+  else if (a.mass)
+    e = launch_pdl(attend_main_kernel<D, GR, true>, dim3(most_segments(seg_grid, p.ni)), dim3(kThreads), bytes, st, 0, a,
+                   sh, tb, p, ws);
   else
-    e = a.mass ? launch_main<D, GR, true>(a, sh, tb, p, ws, st) : launch_main<D, GR, false>(a, sh, tb, p, ws, st);
+    e = launch_pdl(attend_main_kernel<D, GR, false>, dim3(grid), dim3(kThreads), bytes, st, 0, a, sh, tb, p, ws);
   if (e != cudaSuccess || !a.mass) return e;
   return launch_mass(a, tb, p, ws, GR, st);
 }

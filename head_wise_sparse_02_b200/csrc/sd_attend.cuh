@@ -28,6 +28,18 @@ struct Segment {
   long long tile;           // tile0 among all tiles
 };
 
+// CTAs that the shares of ni items aim at when `grid` are resident at once, and
+// the most that they can come to (an item has at least one).
+constexpr int kMaxSegments = 2048;      // or one per item and one more
+__host__ __device__ constexpr int segment_slots(int grid, int ni) {
+  const int waves = (2 * ni + grid - 1) / grid;
+  const long long slots = (long long)grid * (waves > 1 ? waves : 1);
+  return slots < kMaxSegments ? (int)slots : kMaxSegments;
+}
+__host__ __device__ constexpr int most_segments(int grid, int ni) {
+  return segment_slots(grid, ni) > ni + 1 ? segment_slots(grid, ni) : ni + 1;
+}
+
 // Carving of the attend workspace.
 struct AttWs {
   float *partials;          // [(kMaxGrid + ni) slots][GR][D + 2]
@@ -58,7 +70,6 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTileRows = 16;
 constexpr int kMaxGrid = 4096;          // persistent CTAs (partial slots are sized for this)
-constexpr int kMaxSegments = 2048;      // CTAs that take one item each, at most (or one per item and one more)
 constexpr uint32_t kNoRow = 0xFFFFFFFFu; // no cache row (configurations reaching this row number are refused)
 constexpr int kMergeChunk = 64;         // partial slots weighed per step of the final merge
 

@@ -627,10 +627,7 @@ cudaError_t config_t(const AttendArgs *launch, const Shape &sh, const Tables &tb
   *grid = std::min(kMaxSegments, resident_ctas(attend_kv4_kernel<D, GR, MASS>, kThreads4, bytes));
   if (!launch) return cudaSuccess;
   if (*grid <= 0) return cudaErrorInvalidConfiguration;
-  // the layout's bound on the shares (item_segments)
-  const int waves = std::max(1, (2 * p.ni + *grid - 1) / *grid);
-  const int ctas = (int)std::max<long long>(std::min<long long>((long long)*grid * waves, kMaxSegments), p.ni + 1);
-  return launch_pdl(attend_kv4_kernel<D, GR, MASS>, dim3(ctas), dim3(kThreads4), bytes, st, 0, *launch, sh, tb, p, *ws, gr);
+  return launch_pdl(attend_kv4_kernel<D, GR, MASS>, dim3(most_segments(*grid, p.ni)), dim3(kThreads4), bytes, st, 0, *launch, sh, tb, p, *ws, gr);
 }
 
 template <int D, bool MASS>
