@@ -122,14 +122,17 @@ __device__ void item_prefix(const AttendArgs &a, const Shape &sh, const Tables &
 // gets ceil(t_i / per) CTAs, each an equal part of it, with `per` just large
 // enough that all fit the grid.  `grid` CTAs are resident at once; many items take
 // several times that, so that an item of average size still has more than one CTA.
-constexpr int kMinSegTiles = 8;         // tiles a CTA takes at least (two per warp) before an item gets another
+// A CTA takes at least this many tiles before an item gets another: twice as many
+// of the 4-bit tiles, which are a third of the bytes (B 4, 32K: 28.4 us at 8, 26.0
+// at 16, 28.0 at 32; bf16 with weights, B 3, 2K: 23.8 at 8, 32.2 at 16).
+constexpr int kMinSegTiles = 8, kMinSegTiles4 = 16;
 
 template <typename T>
-__device__ __forceinline__ T tiles_per_segment(T W, int ni, int grid) {
+__device__ __forceinline__ T tiles_per_segment(T W, int ni, int grid, int min_tiles) {
   const int slots = segment_slots(grid, ni);
   const T room = slots > ni ? slots - ni : 1;
   const T per = (W + room - 1) / room;
-  return per > kMinSegTiles ? per : T(kMinSegTiles);
+  return per > min_tiles ? per : T(min_tiles);
 }
 
 // CTA c's share: of the item whose CTAs start at first(i) (ascending), with its
@@ -180,7 +183,7 @@ __device__ void item_segments(const AttParams &ap, const AttWs &ws, int grid) {
   __shared__ int wsum[32];
   const int tid = threadIdx.x;
   __syncthreads();
-  const long long per = tiles_per_segment<long long>(ws.tstart[ap.ni], ap.ni, grid);
+  const long long per = tiles_per_segment<long long>(ws.tstart[ap.ni], ap.ni, grid, ap.min_tiles);
   int carry = 0;
   for (int base = 0; base < ap.ni; base += blockDim.x) {
     const int i = base + tid;
@@ -241,7 +244,7 @@ __device__ void item_layout(const AttendArgs &a, const Shape &sh, const Tables &
   }
   if (tid == 0) ws.tstart[ap.ni] = tstart[ap.ni] = W;
   if (seg_grid > 0) {
-    const uint32_t per = tiles_per_segment<uint32_t>(W, ap.ni, seg_grid);
+    const uint32_t per = tiles_per_segment<uint32_t>(W, ap.ni, seg_grid, ap.min_tiles);
     uint32_t total;
     const uint32_t c0 = block_prefix<uint32_t>((nt + per - 1) / per, wsum, total);
     if (tid < ap.ni) first[tid] = (int)c0;
@@ -1014,7 +1017,8 @@ cudaError_t launch_attend(const AttendArgs &a, const Shape &sh, const Tables &tb
                           const uint32_t *plan_only) {
   if (a.batch == 0) return cudaSuccess;
   const AttLayout L = att_layout(sh, tb, a.batch, (long long)a.num_sinks + a.window);
-  const AttParams p = att_params(sh, tb, a.batch);
+  AttParams p = att_params(sh, tb, a.batch);
+  p.min_tiles = a.kv4 ? kMinSegTiles4 : kMinSegTiles;
   char *base = static_cast<char *>(a.ws);
   AttWs ws{};
   ws.partials = reinterpret_cast<float *>(base + L.partials);

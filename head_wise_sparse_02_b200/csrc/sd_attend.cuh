@@ -16,6 +16,7 @@ struct AttParams {
   int ns;                   // plan: spans per sequence
   int n_ret_items;          // B * n_ret retrieval items, numbered first
   int ni;                   // all items: then B * n_loc local items
+  int min_tiles;            // tiles a CTA takes at least before an item gets another (Segment)
 };
 
 // A CTA's share of one item, for a main kernel whose CTAs take one item each
