@@ -45,7 +45,7 @@ namespace {
 
 constexpr int kWarps4 = 4;
 constexpr int kThreads4 = kWarps4 * 32;
-constexpr int kRing4 = 4;               // tiles in flight per warp
+constexpr int kRing4 = 2;               // tiles in flight per warp (B 16, 128K, 2%: 70.8 us; 3: 73.5, 4: 74.1)
 constexpr float kLazy = 4.0f;           // a head's reference may lag its maximum by this (log2)
 constexpr int kScaleTop = 10;           // exponent of the largest p s at p = 1
 // the nibbles at bits 0-3 (low) and 4-7 (high) of both halves of w, as f16: code - 8
@@ -129,9 +129,12 @@ __device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_ui
 //                         column order, value codes [16][d / 2], scales [16][d / 4]]
 //                        [head masks of the tiles, in column order: kWarps4 x kRing4 x 16 x uint16]
 //                        [span prefix of the current item: ns + 1 ints]
-// between items the ring holds the warps' (m, l, acc) for the CTA merge
+// at the end the ring holds the warps' (m, l, acc) for the CTA merge.
+// CTAs per SM: 3 of up to four heads (4, with fewer registers: 78 us instead of
+// 71 at B 16, 128K), 4 of up to eight (3: 72.4 instead of 70.7 us on a ragged batch
+// of 33), 2 of sixteen.
 template <int D, int GR, bool MASS>
-__global__ void __launch_bounds__(kThreads4, GR > 8 ? 2 : 3)
+__global__ void __launch_bounds__(kThreads4, GR > 8 ? 2 : GR > 4 ? 4 : 3)
 attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const AttParams ap, const AttWs ws, int gr) {
   constexpr int NG = D / kKv4Group;                  // groups of channels
   constexpr int kRec = kv4_record_bytes(D);
