@@ -128,7 +128,8 @@ __device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_ui
 // dynamic shared memory: [ring: kWarps4 x kRing4 tiles: key codes [16][d / 2] in
 //                         column order, value codes [16][d / 2], scales [16][d / 4]]
 //                        [head masks of the tiles, in column order: kWarps4 x kRing4 x 16 x uint16]
-//                        [span prefix of the current item: ns + 1 ints]
+//                        [span prefix of the item: ns + 1 ints, rounded up to 16 bytes]
+//                        [query fragments: d / 32 x 2 x 32 lanes x 16 bytes]
 // at the end the ring holds the warps' (m, l, acc) for the CTA merge.
 // CTAs per SM: 3 of up to four heads (4, with fewer registers: 78 us instead of
 // 71 at B 16, 128K), 4 of up to eight (3: 72.4 instead of 70.7 us on a ragged batch
@@ -215,6 +216,10 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
   // ---- queries: A fragments (heads on M; k = the channels of the record's
   // words: lane tq holds channels 8 tq .. 8 tq + 7 of every group, nibble pairs
   // (i, i + 4)), and the sums over the groups' channels; all times 2^k
+  // The fragments wait in shared memory (all warps have the same): as registers they
+  // would have to be copied side by side, with the zeros of the unused rows, for
+  // every product.
+  uint4 *qf = reinterpret_cast<uint4 *>(pre + ((ap.ns + 1 + 3) & ~3));   // [NG][2][32 lanes]
   uint32_t qa[NG][2][HB][2];
   float qs[HB][NG], qsc[HB];
 #pragma unroll
@@ -250,6 +255,14 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
       qs[hb][g] = sum * f;
     }
   }
+  if (warp == 0)
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+        qf[(g * 2 + ks) * 32 + lane] = make_uint4(qa[g][ks][0][0], HB == 2 ? qa[g][ks][HB - 1][0] : 0u, qa[g][ks][0][1],
+                                                  HB == 2 ? qa[g][ks][HB - 1][1] : 0u);
+  __syncthreads();
   float m[HB], l[HB], o[HB][NG][2][4];
   float2 olo[HB][NG], oup[HB][NG];                   // sums of p lo and of 8 p s 2^-R, two partial sums each
   uint32_t nf[NG / 2], thr[NG / 2];                  // bf16 pairs: 2^-R_g, and the largest s it serves
@@ -371,15 +384,14 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         float s[4];
+        const uint4 qa0 = qf[(g * 2) * 32 + lane], qa1 = qf[(g * 2 + 1) * 32 + lane];
 #pragma unroll
         for (int u = 0; u < (PACK ? 2 : 1); ++u) {
           const uint32_t w = kw[PACK ? u : jj][g], w8 = w >> 8;
           const uint32_t b0 = low_codes(w), b1 = high_codes(w), b2 = low_codes(w8), b3 = high_codes(w8);
-          const uint32_t a1 = HB == 2 ? qa[g][0][HB - 1][0] : 0u, a3 = HB == 2 ? qa[g][0][HB - 1][1] : 0u;
-          const uint32_t c1 = HB == 2 ? qa[g][1][HB - 1][0] : 0u, c3 = HB == 2 ? qa[g][1][HB - 1][1] : 0u;
           float t[4];
-          mma_f16_first(t, qa[g][0][0][0], a1, qa[g][0][0][1], a3, b0, b1);
-          mma_f16(t, qa[g][1][0][0], c1, qa[g][1][0][1], c3, b2, b3);
+          mma_f16_first(t, qa0.x, qa0.y, qa0.z, qa0.w, b0, b1);
+          mma_f16(t, qa1.x, qa1.y, qa1.z, qa1.w, b2, b3);
           if (u == 0) {
             s[0] = t[0]; s[1] = t[1]; s[2] = t[2]; s[3] = t[3];
           } else {
@@ -621,7 +633,7 @@ template <int D, int GR, bool MASS>
 cudaError_t config_t(const AttendArgs *launch, const Shape &sh, const Tables &tb, const AttParams &p, const AttWs *ws,
                      int gr, cudaStream_t st, int *grid) {
   const size_t ring = (size_t)kWarps4 * kRing4 * kTileRows * kv4_record_bytes(D);
-  const size_t lists = (size_t)kWarps4 * kRing4 * kTileRows * 2 + (size_t)(p.ns + 1) * 4;
+  const size_t lists = (size_t)kWarps4 * kRing4 * kTileRows * 2 + (size_t)((p.ns + 1 + 3) & ~3) * 4 + (size_t)(D / 32) * 2 * 32 * 16;
   const size_t merge = std::max((size_t)kWarps4 * 32 * 4 + (size_t)kWarps4 * GR * D * 4,
                                 (size_t)GR * (kMergeChunk + 2) * 4);
   const size_t bytes = std::max(ring + lists, merge);
