@@ -804,7 +804,7 @@ attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
         split_bf16(p[1][0], p[1][1], ph[2], pl[2]);  // head gq,     rows 8+2tq, 9+2tq
         split_bf16(p[1][2], p[1][3], ph[3], pl[3]);  // head gq + 8, rows 8+2tq, 9+2tq
         // with accumulated weights the outputs take a third term, so that they are
-        // as exact as the weights (2.5e-7 instead of 1.4e-6 of the output)
+        // as exact as the weights
         [[maybe_unused]] uint32_t pr[4];
         if constexpr (MASS) {
           pr[0] = rest_bf16(p[0][0], p[0][1], ph[0], pl[0]);
@@ -816,25 +816,41 @@ attend_main_kernel(const AttendArgs a, const Shape sh, const Tables tb, const At
         for (int nn = 0; nn < NT; nn += 2) {
           uint32_t vb[4];
           ldsm_x4_t(vb, kt + v_lane + nn * 16);
-          if constexpr (HI) {
+          if constexpr (MASS) {
+            // the tile's sum by itself, the smallest terms first, then added in
+            // float32: the tensor cores truncate what they add to an accumulator,
+            // which over 18 tiles cost 1.1e-6 of the output
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float u[4] = {0.f, 0.f, 0.f, 0.f};
+              if constexpr (HI) {
+                mma_bf16(u, pr[0], pr[1], pr[2], pr[3], vb[2 * e], vb[2 * e + 1]);
+                mma_bf16(u, pl[0], pl[1], pl[2], pl[3], vb[2 * e], vb[2 * e + 1]);
+                mma_bf16(u, ph[0], ph[1], ph[2], ph[3], vb[2 * e], vb[2 * e + 1]);
+                o[nn + e][2] += u[2];
+                o[nn + e][3] += u[3];
+              } else {
+                float t[2] = {zf, zf};
+                mma_bf16_top(t, pr[0], pr[2], vb[2 * e], vb[2 * e + 1], zu, zf);
+                mma_bf16_top(t, pl[0], pl[2], vb[2 * e], vb[2 * e + 1], zu, zf);
+                mma_bf16_top(t, ph[0], ph[2], vb[2 * e], vb[2 * e + 1], zu, zf);
+                u[0] = t[0];
+                u[1] = t[1];
+              }
+              o[nn + e][0] += u[0];
+              o[nn + e][1] += u[1];
+            }
+          } else if constexpr (HI) {
             mma_bf16(o[nn], ph[0], ph[1], ph[2], ph[3], vb[0], vb[1]);
             mma_bf16(o[nn], pl[0], pl[1], pl[2], pl[3], vb[0], vb[1]);
             mma_bf16(o[nn + 1], ph[0], ph[1], ph[2], ph[3], vb[2], vb[3]);
             mma_bf16(o[nn + 1], pl[0], pl[1], pl[2], pl[3], vb[2], vb[3]);
-            if constexpr (MASS) {
-              mma_bf16(o[nn], pr[0], pr[1], pr[2], pr[3], vb[0], vb[1]);
-              mma_bf16(o[nn + 1], pr[0], pr[1], pr[2], pr[3], vb[2], vb[3]);
-            }
           } else {
             float u0[2] = {o[nn][0], o[nn][1]}, u1[2] = {o[nn + 1][0], o[nn + 1][1]};
             mma_bf16_top(u0, ph[0], ph[2], vb[0], vb[1], zu, zf);
             mma_bf16_top(u0, pl[0], pl[2], vb[0], vb[1], zu, zf);
             mma_bf16_top(u1, ph[0], ph[2], vb[2], vb[3], zu, zf);
             mma_bf16_top(u1, pl[0], pl[2], vb[2], vb[3], zu, zf);
-            if constexpr (MASS) {
-              mma_bf16_top(u0, pr[0], pr[2], vb[0], vb[1], zu, zf);
-              mma_bf16_top(u1, pr[0], pr[2], vb[2], vb[3], zu, zf);
-            }
             o[nn][0] = u0[0]; o[nn][1] = u0[1]; o[nn + 1][0] = u1[0]; o[nn + 1][1] = u1[1];
           }
         }
