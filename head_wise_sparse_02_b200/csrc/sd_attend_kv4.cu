@@ -7,10 +7,9 @@
 // the tensor cores contract the query with the codes, one accumulator per
 // group, and the scales join in float32.  Likewise
 //   o_i = sum_j (p_j s_jg) (c_ji - 8) + sum_j p_j (lo_jg + 8 s_jg) :
-// the operands are p s and the codes about their middle (sums of either sign:
-// the tensor cores truncate what they add to an accumulator, and a sum of
-// positive terms many times the result would lose 3e-6 of it over 16 tiles), and
-// the second sum is kept per group in float32.
+// the operands are p s and the codes about their middle (the tensor cores truncate
+// what they add to an accumulator, and sums of positive terms many times the
+// result lose the most), and the second sum is kept per group in float32.
 //
 // Everything is contracted in f16, where a code is two instructions away: the
 // four bits of a nibble put at bits 0-3 or 4-7 of f16's 1024 are 1024 + c or
@@ -101,6 +100,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 r;
   asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d;}\n"
       : "=f"(r.x), "=f"(r.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
@@ -264,7 +270,7 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
                                                   HB == 2 ? qa[g][ks][HB - 1][1] : 0u);
   __syncthreads();
   float m[HB], l[HB], o[HB][NG][2][4];
-  float2 olo[HB][NG], oup[HB][NG];                   // sums of p lo and of 8 p s 2^-R, two partial sums each
+  float2 olo[HB][NG];                                // two partial sums each
   uint32_t nf[NG / 2], thr[NG / 2];                  // bf16 pairs: 2^-R_g, and the largest s it serves
 #pragma unroll
   for (int w = 0; w < NG / 2; ++w) {
@@ -277,7 +283,7 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
     l[hb] = 0.0f;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      olo[hb][g] = oup[hb][g] = make_float2(0.0f, 0.0f);
+      olo[hb][g] = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) o[hb][g][mt][0] = o[hb][g][mt][1] = o[hb][g][mt][2] = o[hb][g][mt][3] = 0.0f;
     }
@@ -492,7 +498,6 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
         for (int g = 0; g < NG; ++g) {
           olo[hb][g] = mul2(olo[hb][g], make_float2(al, al));
           const float r = rf[g];
-          oup[hb][g] = mul2(oup[hb][g], make_float2(al * r, al * r));
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
             o[hb][g][mt][0] *= a0 * r;
@@ -549,8 +554,10 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
 #pragma unroll
           for (int jj = 0; jj < NJ; ++jj) {
             const float2 ps = mul2(x[hb][jj], halves(vn[jj][0], vn[jj][1], i));
-            olo[hb][g] = fma2(x[hb][jj], halves(vl[jj][0][w], vl[jj][1][w], i), olo[hb][g]);
-            oup[hb][g] = fma2(ps, make_float2(8.0f, 8.0f), oup[hb][g]);
+            // lo and 8 s nearly cancel: joined first, so that the sum keeps its precision
+            const float2 mid = fma2(halves(vs[jj][0][w], vs[jj][1][w], i), make_float2(8.0f, 8.0f),
+                                    halves(vl[jj][0][w], vl[jj][1][w], i));
+            olo[hb][g] = fma2(x[hb][jj], mid, olo[hb][g]);
             bh[jj] = pack_f16(ps.x, ps.y);
             const float2 h = unpack_f16(bh[jj]);
             bl[jj] = pack_f16(ps.x - h.x, ps.y - h.y);
@@ -564,8 +571,21 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
           }
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
-            mma_f16(o[hb][g][mt], A[mt][0], A[mt][1], A[mt][2], A[mt][3], bh[0], bh[1]);
-            if constexpr (!PACK) mma_f16(o[hb][g][mt], A[mt][0], A[mt][1], A[mt][2], A[mt][3], bl[0], bl[1]);
+            // the tile's sum by itself, then added in float32 (the accumulators of
+            // the tensor cores truncate: over 150 tiles 1.7e-5 of the output)
+            float u[4];
+            if constexpr (PACK) {
+              mma_f16_first(u, A[mt][0], A[mt][1], A[mt][2], A[mt][3], bh[0], bh[1]);
+            } else {
+              mma_f16_first(u, A[mt][0], A[mt][1], A[mt][2], A[mt][3], bl[0], bl[1]);
+              mma_f16(u, A[mt][0], A[mt][1], A[mt][2], A[mt][3], bh[0], bh[1]);
+            }
+            const float2 s0 = add2(make_float2(o[hb][g][mt][0], o[hb][g][mt][1]), make_float2(u[0], u[1]));
+            const float2 s1 = add2(make_float2(o[hb][g][mt][2], o[hb][g][mt][3]), make_float2(u[2], u[3]));
+            o[hb][g][mt][0] = s0.x;
+            o[hb][g][mt][1] = s0.y;
+            o[hb][g][mt][2] = s1.x;
+            o[hb][g][mt][3] = s1.y;
           }
         }
       }
@@ -590,8 +610,7 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
     l[hb] = shared(l[hb]);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const float un = 1.0f / ((g & 1) ? bf16_hi(nf[g / 2]) : bf16_lo(nf[g / 2]));   // 2^R: exact
-      olo[hb][g].x = shared(fmaf(oup[hb][g].x + oup[hb][g].y, un, olo[hb][g].x + olo[hb][g].y));
+      olo[hb][g].x = shared(olo[hb][g].x + olo[hb][g].y);
     }
   }
   __syncthreads();                                   // ring no longer read
