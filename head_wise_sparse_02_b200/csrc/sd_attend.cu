@@ -985,8 +985,8 @@ cudaError_t launch_t(const AttendArgs &a, const Shape &sh, const Tables &tb, con
     if (e != cudaSuccess) return e;
   }
   const int seg_grid = a.kv4 || a.mass ? std::min(grid, kMaxSegments) : 0;
-  e = launch_pdl(attend_prefix_kernel<D>, dim3(1), dim3(std::min(1024, std::max(128, pow2_ceil(p.ni)))), 0, st, 0, a, sh, tb, p, ws,
-                 seg_grid);
+  const int layout_threads = p.ni <= 64 ? 128 : std::min(1024, std::max(256, pow2_ceil(p.ni)));
+  e = launch_pdl(attend_prefix_kernel<D>, dim3(1), dim3(layout_threads), 0, st, 0, a, sh, tb, p, ws, seg_grid);
   if (e != cudaSuccess) return e;
   if (a.kv4)
     e = launch_attend_kv4_main(a, sh, tb, p, ws, GR, st);
