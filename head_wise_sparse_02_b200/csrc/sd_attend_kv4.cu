@@ -304,7 +304,7 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
     const int gx = r0 + (warp + q * kWarps4) * kTileRows + crow;
     if (gx >= r1) return;
     if (is_ret) {
-      while (pre[sp + 1] <= gx) ++sp;                // ends: gx < rows of the item = pre[ns_item]
+      while (sp + 1 < ns_item && pre[sp + 1] <= gx) ++sp;
       const int e = sp * ap.span + (gx - pre[sp]);
       row = __ldcg(prow + e);
       mask = __ldcg(pmask + e);

@@ -318,14 +318,14 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
 // chunk x % total of row x / total (by a multiplication: x < 2^13, total <= 64).
 template <int ROWS>
 __global__ void __launch_bounds__(kMoveThreads)
-evict_move_kernel(const EvictArgs a, const Shape sh, int total, uint32_t inverse) {
+evict_move_kernel(const EvictArgs a, const Shape sh, int per_item, int total, uint32_t inverse) {
   __shared__ uint32_t src[ROWS], dst[ROWS];
   const int tid = threadIdx.x;
-  const int item = blockIdx.x, b = item / sh.Hkv, g = item % sh.Hkv;
+  const int item = blockIdx.x / per_item, b = item / sh.Hkv, g = item % sh.Hkv;
   pdl_wait();
   pdl_trigger();
   const int keep = std::min((int)clamped_len(a, sh, b), a.budget);
-  const int i0 = blockIdx.y * ROWS;
+  const int i0 = (blockIdx.x - item * per_item) * ROWS;
   const int n = keep - i0 < ROWS ? keep - i0 : ROWS;
   if (n <= 0) return;
   if (tid < n) {
@@ -389,8 +389,11 @@ cudaError_t launch_move(const EvictArgs &a, const Shape &sh, cudaStream_t st) {
       done[dev] = true;
     }
   }
-  return launch_pdl(evict_move_kernel<ROWS>, dim3((unsigned)(a.batch * sh.Hkv), (unsigned)((a.budget + ROWS - 1) / ROWS)),
-                    dim3(kMoveThreads), 0, st, 0, a, sh, total, inverse);
+  const int per_item = (a.budget + ROWS - 1) / ROWS;
+  const long long ctas = (long long)a.batch * sh.Hkv * per_item;
+  if (ctas > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  return launch_pdl(evict_move_kernel<ROWS>, dim3((unsigned)ctas), dim3(kMoveThreads), 0, st, 0, a, sh, per_item, total,
+                    inverse);
 }
 
 template <bool KEYS>

@@ -726,7 +726,8 @@ class SparseDecode:
                           workspace, mass=None, stream=None):
         self._step(q, page_table)
         self._own(kv4_cache.shape, self._records, "kv4_cache")
-        self._own(index_cache.shape, self._index_rows, "index_cache")
+        if index_cache is not None:                          # None without retrieval heads
+            self._own(index_cache.shape, self._index_rows, "index_cache")
         sparse_decode_select_attend_kv4(self.handle, q_pre, q, index_cache, kv4_cache, page_table, seq_lens, sel_idx,
                                         sel_count, out, workspace, mass, stream)
 

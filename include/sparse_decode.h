@@ -529,6 +529,8 @@ SD_API sd_status sparse_decode_kv4_load(sd_ctx *ctx, const void *kv4_cache, cons
  *
  * Records that no append has written may hold NaN scales; they must not be
  * inside any head's set.
+ * Queries, keys and values are below 2^100 in magnitude
+ * (beyond, the kernel's powers of two overflow).
  */
 SD_API sd_status sparse_decode_attend_kv4(sd_ctx *ctx, const void *q, const void *kv4_cache,
                                    const int32_t *page_table, const int32_t *seq_lens, int batch,

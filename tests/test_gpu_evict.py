@@ -101,6 +101,8 @@ CASES = [
     ([6000], 2500, 4, 0, 1, 64, "close"),
     ([3000, 64], 1001, 2, 9, 2, 128, "inf"),
     ([70001, 40000], 5003, 4, 1024, 1, 64, "heavy"),
+    ([200003], 30011, 4, 100, 1, 64, "heavy"),         # more positions than a warp keeps pages for
+    ([300007, 5], 40001, 0, 0, 1, 64, "ties"),         # keys read again from memory
     ([20011] * 6, 15000, 4, 512, 2, 64, "ties"),       # most rows stay; move CTAs of 128 rows
 ]
 

@@ -276,6 +276,8 @@ SHAPES = [
     ("all local", [700, 31], 4, 2, 128, [0] * 8, 1000, 4),
     ("many tiles", [5003, 1200], 4, 2, 128, [1] * 8, 0, 0),
     ("many tiles d64", [4099], 2, 1, 64, [1, 0], 900, 4),
+    ("no tokens at all", [0, 0], 4, 2, 128, [1] * 4 + [0] * 4, 3, 1),
+    ("a share per item", [1 + 5 * (i % 3) for i in range(300)], 1, 8, 64, [1, 0] * 4, 3, 1),
     ("many items", [7 + 11 * (i % 5) for i in range(160)], 2, 8, 64, [1] * 8 + [0] * 8, 9, 1),
 ]
 
@@ -305,6 +307,29 @@ def test_attention_over_wide_ranges(kw, d, G):
     c = Case([2500, 700], G, 1, d, [1] * (G - 1) + [0], 300, 4, seed=G + d, frac=0.6, **kw)
     c.run("kv4", True)
     c.check("kv4", True, str(kw))
+    c.sd.close()
+
+
+def test_dense_sums_over_many_tiles_keep_their_precision():
+    """Every head over 20000 rows: the outputs are a few hundredths of the values they
+    average.  The codes about their middle and the middles themselves sum to values
+    of the outputs' own size, so each of a warp's at most 100 additions of a tile
+    rounds by at most 2^-24 of it: 6e-6 if all fell the same way.  Roundings to
+    nearest do not, and the weights' own errors (4e-7) are independent too, so the
+    2-norm over all outputs stays below 5e-6 of theirs."""
+    n, Hkv, d = 20000, 4, 128
+    c = Case([n, n], 4, Hkv, d, [0] * 16, n, 0, seed=77)
+    c.run("kv4", False)
+    torch.cuda.synchronize()
+    assert c.sd.error_word() == 0
+    out, q = c.out.cpu().numpy().astype(np.float64), c.q.double().cpu().numpy()
+    num = den = 0.0
+    for (b, h), s in c.sets.items():
+        k, v = c.k64[c.start[b] + s, h // 4], c.v64[c.start[b] + s, h // 4]
+        want = O.set_weights(q[b, h], k, d ** -0.5) @ v
+        num += ((out[b, h] - want) ** 2).sum()
+        den += (want ** 2).sum()
+    assert np.sqrt(num / den) <= 5e-6, np.sqrt(num / den)
     c.sd.close()
 
 
