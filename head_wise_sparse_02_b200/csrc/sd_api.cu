@@ -585,6 +585,25 @@ sd_status sparse_decode_mass_workspace_size(const sd_ctx *ctx, int batch, size_t
   }
 }
 
+sd_status sparse_decode_mass_clear(sd_ctx *ctx, float *mass, const int32_t *slots, int num_tokens,
+                                   sd_stream stream) {
+  try {
+    if (!ctx) return SD_ERR_INVALID_ARG;
+    if (num_tokens < 0) return fail(ctx, SD_ERR_INVALID_ARG, "num_tokens < 0");
+    if (num_tokens == 0) return SD_OK;
+    if ((long long)num_tokens * ctx->sh.Hkv >= (1LL << 31))
+      return fail(ctx, SD_ERR_UNSUPPORTED, "num_tokens * Hkv reaches 2^31");
+    if (!mass || !slots) return fail(ctx, SD_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(mass)) return fail(ctx, SD_ERR_INVALID_ARG, "mass must be 16-byte aligned");
+    DeviceGuard dg(ctx->device);
+    const cudaError_t e =
+        sd::launch_mass_clear(mass, slots, num_tokens, ctx->sh, ctx->err_d, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SD_OK : cuda_fail(ctx, e, "mass_clear launch");
+  } catch (...) {
+    return SD_ERR_HOST_MEMORY;
+  }
+}
+
 sd_status sparse_decode_kv4_append(sd_ctx *ctx, const void *k_new, const void *v_new, const int32_t *slots,
                                    int num_tokens, void *kv4_cache, sd_stream stream) {
   try {

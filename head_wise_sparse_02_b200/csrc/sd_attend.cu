@@ -32,8 +32,8 @@
 //         stream tiles through per-warp cp.async rings (whole rows per
 //         instruction, padded row pitch; each warp fetches its tiles' rows
 //         from the union lists itself, one tile ahead, so nothing stops the
-//         rings inside an item) and run them on the tensor cores in
-//         the FlashAttention-2 arrangement: S = Q K^T with mma.m16n8k16 (A =
+//         rings inside an item) and run them on the tensor cores with the
+//         scores kept in registers: S = Q K^T with mma.m16n8k16 (A =
 //         the group's bf16 queries, heads on M; B = K rows by ldmatrix), a
 //         masked online softmax per head in base 2, then O += P V with P taken
 //         straight from the S fragments, split exactly into bf16 hi + lo terms

@@ -50,9 +50,8 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveBatch = 4;           // loads in flight per thread
 constexpr int kMoveMany = 1 << 16;      // rows from which a move CTA takes 128 instead of 32
 
-__device__ __forceinline__ long long clamped_len(const EvictArgs &a, const Shape &sh, int b) {
-  const long long N = a.seq_lens[b];
-  return N < 0 ? 0 : std::min<long long>(N, sh.max_len);
+__device__ __forceinline__ int clamped_len(int N, const Shape &sh) {
+  return N < 0 ? 0 : (int)std::min<long long>(N, sh.max_len);
 }
 
 // Order-preserving key of a weight's bits (-0 as +0; a NaN by its sign: above
@@ -87,8 +86,8 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
   const int item = blockIdx.x / C, b = item / sh.Hkv, g = item % sh.Hkv;
   pdl_wait();
   pdl_trigger();
-  const long long N0 = a.seq_lens[b];
-  const int N = (int)clamped_len(a, sh, b);
+  const int N0 = a.seq_lens[b];
+  const int N = clamped_len(N0, sh);
   if (tid == 0 && rank == 0 && g == 0) {
     if (N0 != N) raise_error(a.err, SD_EBIT_SEQLEN);
     a.new_lens[b] = std::min(N, a.budget);
@@ -107,13 +106,19 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
   uint4 *keys4 = reinterpret_cast<uint4 *>(dyn + kBins / C);
   auto keys_at = [&](int j) -> uint4 { return KEYS ? keys4[(j - j0) / 4] : load4(j); };
   uint32_t tau = 0u;
-  int need = 0;                                                  // ties of tau that stay
-  if (!all) {
-    need = a.budget - a.keep_first - a.keep_last;
+  int need = a.budget - a.keep_first - a.keep_last;              // in the end: ties of tau that stay
+  const bool search = need > 0;
+  // The number of cluster barriers does not depend on the lengths or the
+  // weights: a CTA that read another length (seq_lens written meanwhile) would
+  // otherwise leave its cluster waiting.
+  if (search && all) {
+    for (int k = 0; k < 2 * 3; ++k) cl.sync();
+  } else if (search) {
     const int widths[3] = {11, 11, 10};
     uint32_t prefix = 0u, mask = 0u;
     int shift = 32;
-    for (int pass = 0; pass < 3 && need > 0; ++pass) {
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
       const int bits = widths[pass], bins = 1 << bits;
       shift -= bits;
       for (int x = tid; x < bins; x += kKeepThreads) S.hist[x] = 0u;
@@ -160,6 +165,7 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
         uint32_t n = 0u;
         for (int w = 0; w < kKeepWarps; ++w) n += S.wsum[w];
         S.share = n;
+        S.digit = S.above = 0u;                                    // the same in every CTA if no bin is found below
       }
       cl.sync();                                                 // every histogram read, every share summed
       // the share that holds the need-th count from the top, then its bin (lane r
@@ -171,7 +177,9 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
         const uint32_t y = __shfl_up_sync(kFull, upto, o);
         if (lane >= o) upto += y;
       }
-      const int owner = __ffs(__ballot_sync(kFull, upto >= (uint32_t)need)) - 1;   // below C: the shares hold need
+      const unsigned enough = __ballot_sync(kFull, upto >= (uint32_t)need);
+      // the shares hold need, unless weights read again have changed under the call
+      const int owner = enough ? __ffs(enough) - 1 : 0;
       const uint32_t before = __shfl_sync(kFull, upto - mine_r, owner);
       const uint32_t *sum = cl.map_shared_rank(sums, owner);
       uint32_t mine[kBins / kKeepThreads];
@@ -209,7 +217,7 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
     tau = prefix;
   }
   __syncthreads();                                               // every thread's keys
-  const bool some = !all && a.budget - a.keep_first - a.keep_last > 0;
+  const bool some = search && !all;
   // of the positions j .. j + 3: how many stay outright (low half) and are ties
   // of tau (high half), and which (bits 0-3 and 4-7 of `bits`)
   auto count4 = [&](int j, uint32_t &bits, uint4 &k4) -> uint32_t {
@@ -289,7 +297,8 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const bool one = bits & (1u << u), tie = bits & (16u << u);
-      at[u] = one || (tie && e1 < (uint32_t)need) ? (int)(g1 + std::min(e1, (uint32_t)need)) : -1;
+      const uint32_t to = g1 + std::min(e1, (uint32_t)need);       // below the budget (unless, as above)
+      at[u] = (one || (tie && e1 < (uint32_t)need)) && to < (uint32_t)a.budget ? (int)to : -1;
       if (paged) {
         const int o = at[u] >= 0 ? at[u] / kPage - page0 : 0;
         const int lo = __shfl_sync(kFull, npage0, o & 31), hi = __shfl_sync(kFull, npage1, o & 31);
@@ -324,7 +333,7 @@ evict_move_kernel(const EvictArgs a, const Shape sh, int per_item, int total, ui
   const int item = blockIdx.x / per_item, b = item / sh.Hkv, g = item % sh.Hkv;
   pdl_wait();
   pdl_trigger();
-  const int keep = std::min((int)clamped_len(a, sh, b), a.budget);
+  const int keep = std::min(clamped_len(a.seq_lens[b], sh), a.budget);
   const int i0 = (blockIdx.x - item * per_item) * ROWS;
   const int n = keep - i0 < ROWS ? keep - i0 : ROWS;
   if (n <= 0) return;

@@ -315,6 +315,7 @@ struct AttendArgs {
 constexpr int kKv4Group = 32;
 __host__ __device__ constexpr int kv4_record_bytes(int d) { return d + d / 4; }
 
+cudaError_t launch_mass_clear(float *mass, const int32_t *slots, int T, const Shape &sh, unsigned *err, cudaStream_t st);
 cudaError_t launch_kv4_append(const uint16_t *k_new, const uint16_t *v_new, const int32_t *slots, int T,
                               uint8_t *kv4, const Shape &sh, unsigned *err, cudaStream_t st);
 cudaError_t launch_kv4_load(const uint8_t *kv4, const int32_t *slots, int T, uint16_t *k_out, uint16_t *v_out,

@@ -1,5 +1,5 @@
 // Accumulated attention weights: the pass after an attention call that keeps
-// them.
+// them, and the zeros that new tokens start from.
 //
 //   mass[row(j), g] += sum over the heads h of KV group g that attend to j of
 //                      p_h(j),  p_h(j) = 2^(x_h(j) - m_h) / l_h
@@ -50,7 +50,31 @@ mass_kernel(const AttWs ws, const Group *__restrict__ ret, const Group *__restri
   }
 }
 
+// One thread per (token, KV head): the slots new tokens take start from zero
+__global__ void __launch_bounds__(kMassThreads)
+mass_clear_kernel(float *__restrict__ mass, const int32_t *__restrict__ slots, int T, const Shape sh, unsigned *err) {
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t x = blockIdx.x * kMassThreads + threadIdx.x;
+  const int t = (int)(x / (uint32_t)sh.Hkv), g = (int)(x - (uint32_t)t * sh.Hkv);
+  if (t >= T) return;
+  const int slot = __ldg(slots + t);
+  if (slot < 0 || slot / kPage >= sh.num_pages) {
+    if (g == 0) raise_error(err, SD_EBIT_SLOT);
+    return;
+  }
+  mass[((long long)(slot / kPage) * sh.Hkv + g) * kPage + slot % kPage] = 0.0f;
+}
+
 }  // namespace
+
+cudaError_t launch_mass_clear(float *mass, const int32_t *slots, int T, const Shape &sh, unsigned *err,
+                              cudaStream_t st) {
+  if (T == 0) return cudaSuccess;
+  const long long n = (long long)T * sh.Hkv;                     // below 2^31
+  return launch_pdl(mass_clear_kernel, dim3((unsigned)((n + kMassThreads - 1) / kMassThreads)), dim3(kMassThreads), 0, st,
+                    0, mass, slots, T, sh, err);
+}
 
 cudaError_t launch_mass(const AttendArgs &a, const Tables &tb, const AttParams &p, const AttWs &ws, int gr,
                         cudaStream_t st) {

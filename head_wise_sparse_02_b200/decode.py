@@ -3,11 +3,21 @@ tokens, select, attend.  Torch is used only to hold device buffers."""
 
 from __future__ import annotations
 
+import contextlib
 from typing import Optional, Sequence
 
 import torch
 
 from .sparse_decode import SparseDecode
+
+
+def _on(stream):
+    """Torch's own operations on the stream that the calls are given (None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream))
+    return torch.cuda.stream(stream)
 
 
 class DecodeStep:
@@ -40,6 +50,7 @@ class DecodeStep:
         self.workspace, self.sel_idx, self.sel_count = self.sd.alloc(self.batch)
         self.out = torch.empty((self.batch, num_q_heads, d), dtype=torch.float32, device=dev)
         self.kv4: Optional[torch.Tensor] = None                         # 4-bit records (make_kv4)
+        self.k_ret: Optional[torch.Tensor] = None                       # split layout (make_split)
         self.mass: Optional[torch.Tensor] = None                        # accumulated weights (keep_mass)
 
     def build_index(self, slots: torch.Tensor, keys: torch.Tensor, stream=None):
@@ -73,6 +84,8 @@ class DecodeStep:
         """One decode step: index the appended tokens, then select and attend."""
         if new_keys is not None:
             self.sd.index_keys(new_keys, new_slots, self.index_cache, stream)
+            if self.mass is not None:
+                self.sd.mass_clear(self.mass, new_slots, stream)
         return self.select_attend(q_pre, q, stream)
 
     # ---- split layout: paged caches of the retrieval groups, compacted local caches
@@ -134,12 +147,13 @@ class DecodeStep:
     def make_kv4(self, stream=None):
         """Build the cache of 4-bit records from the full caches (every cached token)."""
         self.kv4 = self.sd.kv4_cache()
-        _, _, slot = self._positions()
-        for at in range(0, slot.numel(), 1 << 16):                      # bounded copies of the rows
-            s = slot[at:at + (1 << 16)]
-            k = self.k_cache[s // 16, :, s % 16].contiguous()
-            v = self.v_cache[s // 16, :, s % 16].contiguous()
-            self.sd.kv4_append(k, v, s.to(torch.int32), self.kv4, stream)
+        with _on(stream):
+            _, _, slot = self._positions()
+            for at in range(0, slot.numel(), 1 << 16):                  # bounded copies of the rows
+                s = slot[at:at + (1 << 16)]
+                k = self.k_cache[s // 16, :, s % 16].contiguous()
+                v = self.v_cache[s // 16, :, s % 16].contiguous()
+                self.sd.kv4_append(k, v, s.to(torch.int32), self.kv4, stream)
 
     def keep_mass(self):
         """Accumulate the attention weights from here on (and size the workspace for it)."""
@@ -169,27 +183,36 @@ class DecodeStep:
 
     def step_kv4(self, q_pre: torch.Tensor, q: torch.Tensor, new_k_pre: torch.Tensor, new_k: torch.Tensor,
                  new_v: torch.Tensor, new_slots: torch.Tensor, stream=None) -> torch.Tensor:
-        """One decode step on the 4-bit cache: append and index the new tokens, then
-        select and attend."""
+        """One decode step on the 4-bit cache: append and index the new tokens (whose
+        accumulated weights, if kept, start from zero), then select and attend."""
         self.sd.kv4_append(new_k, new_v, new_slots, self.kv4, stream)
+        if self.mass is not None:
+            self.sd.mass_clear(self.mass, new_slots, stream)
         self.sd.index_keys(new_k_pre, new_slots, self.index_cache, stream)
         return self.select_attend_kv4(q_pre, q, stream)
 
     def evict(self, new_page_table: torch.Tensor, budget: int, keep_first: Optional[int] = None,
               keep_last: Optional[int] = None, stream=None) -> torch.Tensor:
         """Shorten every sequence to at most `budget` tokens per KV head by accumulated
-        weight and continue on the new pages; the sinks and the window stay by
-        default.  Returns the kept positions [B, Hkv, budget] (entries past a
-        sequence's new length are -1)."""
+        weight and continue on the new pages, with every cache of the full layout;
+        the sinks and the window stay by default.  Returns the kept positions
+        [B, Hkv, budget] (entries past a sequence's new length are -1)."""
+        if self.mass is None:
+            raise RuntimeError("evict needs accumulated weights: call keep_mass first")
+        if self.k_ret is not None:
+            raise RuntimeError("evict does not move the split layout's caches")
         cfg = self.sd.cfg
         first = cfg.get("num_sinks", 0) if keep_first is None else keep_first
         last = cfg.get("window", 0) if keep_last is None else keep_last
-        kept = torch.full((self.batch, self.k_cache.shape[1], budget), -1, dtype=torch.int32,
-                          device=self.k_cache.device)
-        lens = torch.empty_like(self.seq_lens)
-        caches = dict(kv4_cache=self.kv4) if self.kv4 is not None else dict(k_cache=self.k_cache, v_cache=self.v_cache)
-        self.sd.evict(self.mass, self.page_table, self.seq_lens, new_page_table, budget, first, last, kept, lens,
-                      index_cache=self.index_cache, stream=stream, **caches)
+        with _on(stream):
+            kept = torch.full((self.batch, self.k_cache.shape[1], budget), -1, dtype=torch.int32,
+                              device=self.k_cache.device)
+            lens = torch.empty_like(self.seq_lens)
+            self.sd.evict(self.mass, self.page_table, self.seq_lens, new_page_table, budget, first, last, kept, lens,
+                          k_cache=self.k_cache, v_cache=self.v_cache, index_cache=self.index_cache,
+                          kv4_cache=self.kv4, stream=stream)
+            for t in (self.page_table, self.seq_lens):                  # read by this stream until here
+                t.record_stream(torch.cuda.current_stream(t.device))
         self.page_table, self.seq_lens = new_page_table, lens
         return kept
 

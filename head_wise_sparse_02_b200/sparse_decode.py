@@ -63,6 +63,7 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sparse_decode_local_append": (c_int, [P, P, P, P, P, c_int, P, P, P]),
         "sparse_decode_prefill": (c_int, [P, P, P, P, P, P, P, c_int, c_int, P, P]),
         "sparse_decode_mass_workspace_size": (c_int, [P, c_int, POINTER(c_size_t)]),
+        "sparse_decode_mass_clear": (c_int, [P, P, P, c_int, P]),
         "sparse_decode_kv4_append": (c_int, [P, P, P, P, c_int, P, P]),
         "sparse_decode_kv4_load": (c_int, [P, P, P, c_int, P, P, P]),
         "sparse_decode_attend_kv4": (c_int, [P, P, P, P, P, c_int, P, P, c_int, P, P, P, c_size_t, P]),
@@ -506,6 +507,15 @@ def sparse_decode_select_attend_mass(ctx: int, q_pre, q, index_cache, k_cache, v
         _fast(workspace, torch.uint8, "workspace", dev), workspace.numel(), _stream(stream, dev)), ctx)
 
 
+def sparse_decode_mass_clear(ctx: int, mass: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+    """Zero the accumulated weights of the slots that new tokens take."""
+    if mass.dim() != 3:
+        raise ValueError(f"mass must be [num_pages, Hkv, page], got {tuple(mass.shape)}")
+    dev = mass.get_device()
+    _check(LIB.sparse_decode_mass_clear(ctx, _fast(mass, torch.float32, "mass", dev),
+                                        _fast(slots, torch.int32, "slots", dev), slots.numel(), _stream(stream, dev)), ctx)
+
+
 def sparse_decode_evict(ctx: int, mass, page_table, seq_lens, new_page_table, budget: int, keep_first: int,
                         keep_last: int, kept, new_lens, k_cache=None, v_cache=None, index_cache=None, kv4_cache=None,
                         stream=None) -> None:
@@ -744,6 +754,10 @@ class SparseDecode:
         self._own(mass.shape, self._rows, "mass")
         sparse_decode_select_attend_mass(self.handle, q_pre, q, index_cache, k_cache, v_cache, page_table, seq_lens,
                                          sel_idx, sel_count, out, mass, workspace, stream)
+
+    def mass_clear(self, mass, slots, stream=None):
+        self._own(mass.shape, self._rows, "mass")
+        sparse_decode_mass_clear(self.handle, mass, slots, stream)
 
     def evict(self, mass, page_table, seq_lens, new_page_table, budget, keep_first, keep_last, kept, new_lens,
               k_cache=None, v_cache=None, index_cache=None, kv4_cache=None, stream=None):

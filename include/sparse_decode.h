@@ -40,7 +40,8 @@
  *     vector and asynchronous copies); a misaligned one is rejected with
  *     SD_ERR_INVALID_ARG.
  *   - Hot calls (index_keys, local_append, select, attend and their joined,
- *     split, 4-bit and weight-accumulating forms, kv4_append, kv4_load, evict)
+ *     split, 4-bit and weight-accumulating forms, kv4_append, kv4_load,
+ *     mass_clear, evict)
  *     allocate nothing, never synchronise the host, and
  *     enqueue their work on `stream` (a cudaStream_t; NULL = the legacy
  *     default stream).  Argument errors are
@@ -586,6 +587,23 @@ SD_API sd_status sparse_decode_select_attend_mass(sd_ctx *ctx, const void *q_pre
 SD_API sd_status sparse_decode_mass_workspace_size(const sd_ctx *ctx, int batch, size_t *bytes);
 
 /*
+ * sparse_decode_mass_clear -- zero the accumulated weights of new tokens:
+ *
+ *   mass[slots[t] / P, g, slots[t] % P] = 0     for every KV head g
+ *
+ * A slot that a new token takes still holds what was added for the slot's last
+ * token (or, on new pages, what the memory held).
+ *
+ *   mass   device float32 [num_pages, Hkv, P], 16-byte aligned, updated in place.
+ *   slots  device int32 [num_tokens].
+ *
+ * A slot outside the pool sets SD_EBIT_SLOT and is skipped.  num_tokens == 0 is
+ * a no-op; num_tokens * Hkv must stay below 2^31 (SD_ERR_UNSUPPORTED).
+ */
+SD_API sd_status sparse_decode_mass_clear(sd_ctx *ctx, float *mass, const int32_t *slots, int num_tokens,
+                                   sd_stream stream);
+
+/*
  * sparse_decode_evict -- shorten every sequence of the batch to at most `budget`
  * cached tokens per KV head.  Of a sequence with N_b > budget each KV head g
  * keeps, as its own set,
@@ -609,7 +627,7 @@ SD_API sd_status sparse_decode_mass_workspace_size(const sd_ctx *ctx, int batch,
  *                   pages that no sequence of the batch uses, each once (rows of
  *                   a page that is both read and written, or written twice, are
  *                   unspecified).  Slots past n_b - 1 of the last page are left
- *                   as they were.
+ *                   as they were, their weights too (sparse_decode_mass_clear).
  *   kept            device int32 [B, Hkv, budget]: receives j_i; entries past
  *                   n_b - 1 are left as they were.
  *   new_lens        device int32 [B]: receives n_b.  Not the same memory as

@@ -124,6 +124,24 @@ def test_contexts_too_long_for_shared_memory():
     p.sd.close()
 
 
+def test_pages_both_read_and_written_touch_nothing_else():
+    # rows are unspecified then, and weights that the search reads again may have changed
+    p = Pool([300007, 290001], 200003, 2, 64, "heavy", 63)
+    p.new_table = p.table.copy()
+    n = p.kept.numel()
+    room = torch.full((n + 4096,), -7, dtype=torch.int32, device="cuda")
+    p.kept = room[:n].view(p.kept.shape)
+    p.run(4, 100)
+    torch.cuda.synchronize()
+    p.sd.error_word()
+    assert (room[n:] == -7).all() and ((p.kept >= -7) & (p.kept < 300007)).all()
+    assert p.new_lens.tolist() == [200003, 200003]
+    idle = np.setdiff1d(np.arange(p.mass.shape[0]), p.table[p.table >= 0])
+    for k, v in (*p.caches.items(), ("mass", p.mass)):
+        assert torch.equal(v[idle].view(torch.uint8), p.before[k][idle].view(torch.uint8)), k
+    p.sd.close()
+
+
 @pytest.mark.parametrize("names", [(), ("kv4_cache",), ("k_cache", "v_cache"), ("index_cache",), ("v_cache", "kv4_cache")])
 @pytest.mark.parametrize("d", [64, 128])
 def test_any_subset_of_the_caches(names, d):
@@ -286,6 +304,94 @@ def test_decode_loop_appends_attends_accumulates_and_evicts():
         for g in range(Hkv):
             m = _gather(st.mass, st.page_table, b, g, int(st.seq_lens[b]))
             assert np.abs(m - model[b, g]["m"]).max() <= 1e-4
+    st.close()
+
+
+@pytest.mark.parametrize("d,Hkv,T", [(64, 1, 1), (128, 3, 47), (128, 8, 700)])
+def test_new_tokens_start_from_zero_weight(d, Hkv, T):
+    from head_wise_sparse_02_b200.sparse_decode import SD_EBIT_SLOT, SD_ERR_INVALID_ARG, SparseDecodeError
+    pages = (T + 15) // 16 + 3
+    sd = _context([1] * Hkv, Hkv, d, pages, 4, 1)
+    mass = 1 + torch.rand((pages, Hkv, 16), generator=_gen(T), device="cuda")
+    want = mass.clone()
+    slots = torch.randperm(pages * 16, generator=_gen(d), device="cuda")[:T].to(torch.int32)
+    sd.mass_clear(mass, slots[:0])
+    assert torch.equal(mass, want)
+    sd.mass_clear(mass, slots)
+    want[slots.long() // 16, :, slots.long() % 16] = 0
+    assert sd.error_word() == 0 and torch.equal(mass, want)
+    side = torch.cuda.Stream()
+    mass.fill_(2.0)
+    side.wait_stream(torch.cuda.current_stream())
+    sd.mass_clear(mass, torch.tensor([-1, 3, pages * 16, 2 ** 31 - 1], dtype=torch.int32, device="cuda"), stream=side)
+    torch.cuda.synchronize()
+    want.fill_(2.0)
+    want[0, :, 3] = 0
+    assert sd.error_word() == SD_EBIT_SLOT and torch.equal(mass, want)
+    for bad in (mass[1:], mass.double(), mass.cpu()):
+        with pytest.raises((ValueError, TypeError)):
+            sd.mass_clear(bad, slots)
+    with pytest.raises(SparseDecodeError) as e:
+        sd.mass_clear(torch.zeros(mass.numel() + 1, device="cuda")[1:].view(mass.shape), slots)
+    assert e.value.status == SD_ERR_INVALID_ARG
+    sd.close()
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_freed_pages_taken_again(side):
+    """Two evictions, the second onto the first one's old pages: no token appended
+    in between or after inherits a weight, every cache follows the pages, and the
+    split layout is refused.  Bitwise the same on a stream of its own."""
+    from head_wise_sparse_02_b200.decode import DecodeStep
+    B, Hkv, d, budget, maxp = 2, 2, 64, 40, 8
+    pages = 2 * B * maxp
+    perm = torch.randperm(pages, generator=torch.Generator().manual_seed(5)).to(torch.int32).cuda()
+    tables = [perm[:B * maxp].view(B, maxp).contiguous(), perm[B * maxp:].view(B, maxp).contiguous()]
+    k_cache, v_cache = _randn((pages, Hkv, 16, d), 1), _randn((pages, Hkv, 16, d), 2)
+    st = DecodeStep(k_cache=k_cache, v_cache=v_cache, page_table=tables[0],
+                    seq_lens=torch.tensor([90, 61], dtype=torch.int32, device="cuda"), proj=_randn((Hkv, d, 16), 3, 0.1),
+                    num_q_heads=4, head_is_retrieval=[1, 1, 0, 0], window=8, num_sinks=2, mode="top_k", top_k_frac=0.5)
+    with pytest.raises(RuntimeError):
+        st.evict(tables[1], budget)                                     # no weights yet
+    stream = torch.cuda.Stream() if side else None
+    if side:
+        stream.wait_stream(torch.cuda.current_stream())
+    st.make_kv4(stream)
+    torch.cuda.synchronize()
+    st.keep_mass()
+    torch.cuda.synchronize()
+    for turn in (1, 0, 1):
+        for i in range(20):                                            # across a page's end
+            new_k, new_v, q = (_randn((B, h, d), 50 * turn + 3 * i + s) for s, h in ((0, Hkv), (1, Hkv), (2, 4)))
+            n = st.seq_lens.cpu().numpy()
+            slots = torch.tensor([int(st.page_table[b, n[b] // 16]) * 16 + int(n[b]) % 16 for b in range(B)],
+                                 dtype=torch.int32, device="cuda")
+            sl = slots.long()
+            st.mass[sl // 16, :, sl % 16] = 1e6                         # what an earlier token left
+            st.seq_lens.add_(1)
+            torch.cuda.synchronize()
+            st.step_kv4(q, q, new_k, new_k, new_v, slots, stream)
+            torch.cuda.synchronize()
+            assert (st.mass[sl // 16, :, sl % 16] < 2.001).all()         # two heads' weights at most
+        old = {k: getattr(st, k).clone() for k in ("k_cache", "v_cache", "kv4", "index_cache", "mass")}
+        was, lens = st.page_table.cpu().numpy(), st.seq_lens.tolist()
+        torch.cuda.synchronize()
+        kept = st.evict(tables[turn], budget, stream=stream)
+        torch.cuda.synchronize()
+        kept = kept.cpu().numpy()
+        assert st.error_word() == 0 and st.seq_lens.tolist() == [min(x, budget) for x in lens]
+        now = st.page_table.cpu().numpy()
+        for b in range(B):
+            for g in range(Hkv):
+                j = kept[b, g, :min(lens[b], budget)]
+                i = np.arange(j.size)
+                for k, v in old.items():
+                    a = v[was[b, j // 16], g, j % 16]
+                    c = getattr(st, k)[now[b, i // 16], g, i % 16]
+                    assert torch.equal(a.view(torch.uint8), c.view(torch.uint8)), (k, b, g)
+    st.make_split()
+    with pytest.raises(RuntimeError):
+        st.evict(tables[0], budget)
     st.close()
 
 
