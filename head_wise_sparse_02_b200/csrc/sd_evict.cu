@@ -5,14 +5,19 @@
 // 0 .. min(N_b, budget) - 1 of the sequence's new pages.
 //
 // Two launches:
-//   keep  one cluster of CTAs per (b, g), each with a slice of the positions.
+//   keep  one cluster of CTAs per (b, g), each with an equal slice of the
+//         sequence (of the longest possible one instead: 331 against 356 us for
+//         both launches at B 16, ragged to 128K).
 //         The weights become order-preserving 32-bit keys (in shared memory
 //         when the slice fits, else read again from global memory each pass),
 //         and a radix search, 11 bits a pass with the cluster's histograms
 //         summed through distributed shared memory, finds the key tau of the
 //         last weight kept and how many of its ties are.  Positions above tau,
-//         the first ties and the forced ones leave in ascending order.
-//         Bound by instructions: a thread takes four positions at a time (one
+//         the first ties and the forced ones leave in ascending order, gathered
+//         32 at a time so that a lane writes one.
+//         Bound by latency (two cluster barriers and a scan per pass, about 4 us)
+//         and, with many items, by instructions: 40 registers for three CTAs per
+//         SM (two with 64 registers: 322 against 314 us), and a thread takes four positions at a time (one
 //         page lookup and one 16-byte load; a page's weights of a head are 64
 //         bytes), and the zeros, the weights of rows that nothing attended to
 //         and usually the most common value, are counted in a register instead
@@ -73,9 +78,87 @@ struct KeepShared {
   uint32_t wsum[kKeepWarps];
 };
 
+// One step of the search: the digit (bin) of the need-th weight from the top,
+// from the CTAs' histograms S.hist of `bins` counts; need becomes its rank among
+// the weights of that digit.  Two cluster barriers, whatever the counts are.
+__device__ uint32_t search_digit(cg::cluster_group &cl, KeepShared &S, uint32_t *sums, int bins, int &need) {
+  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  cl.sync();
+  // bins of the whole cluster: CTA r sums share r of them (counted from the
+  // highest bin), so that each histogram is read once over the cluster
+  const int share = bins / C;
+  uint32_t tot = 0u;
+  for (int x = tid; x < share; x += kKeepThreads) {
+    const int bin = bins - 1 - (rank * share + x);
+    uint32_t n = 0u;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) n += r < C ? cl.map_shared_rank(S.hist, r)[bin] : 0u;
+    sums[x] = n;
+    tot += n;
+  }
+  tot = __reduce_add_sync(kFull, tot);
+  if (lane == 0) S.wsum[warp] = tot;
+  __syncthreads();
+  if (tid == 0) {
+    uint32_t n = 0u;
+    for (int w = 0; w < kKeepWarps; ++w) n += S.wsum[w];
+    S.share = n;
+    S.digit = S.above = 0u;                                      // the same in every CTA if no bin is found below
+  }
+  cl.sync();                                                     // every histogram read, every share summed
+  // the share that holds the need-th count from the top, then its bin (lane r
+  // reads share r, so that the remote reads are one latency)
+  const uint32_t mine_r = lane < C ? *cl.map_shared_rank(&S.share, lane) : 0u;
+  uint32_t upto = mine_r;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(kFull, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const unsigned enough = __ballot_sync(kFull, upto >= (uint32_t)need);
+  // the shares hold need, unless weights read again have changed under the call
+  const int owner = enough ? __ffs(enough) - 1 : 0;
+  const uint32_t before = __shfl_sync(kFull, upto - mine_r, owner);
+  const uint32_t *sum = cl.map_shared_rank(sums, owner);
+  uint32_t mine[kBins / kKeepThreads];
+  tot = 0u;
+#pragma unroll
+  for (int u = 0; u < kBins / kKeepThreads; ++u) {
+    const int x = tid * (kBins / kKeepThreads) + u;
+    mine[u] = x < share ? sum[x] : 0u;
+    tot += mine[u];
+  }
+  uint32_t incl = tot;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();                                               // wsum read
+  if (lane == 31) S.wsum[warp] = incl;
+  __syncthreads();
+  uint32_t run = before + incl - tot;
+  for (int w = 0; w < warp; ++w) run += S.wsum[w];
+#pragma unroll
+  for (int u = 0; u < kBins / kKeepThreads; ++u) {
+    if (run < (uint32_t)need && run + mine[u] >= (uint32_t)need) {         // exactly one thread
+      S.digit = (uint32_t)(bins - 1 - (owner * share + tid * (kBins / kKeepThreads) + u));
+      S.above = run;
+    }
+    run += mine[u];
+  }
+  __syncthreads();
+  need -= (int)S.above;
+  return S.digit;
+}
+
 // dynamic shared memory: [cluster sums of this CTA's share of the bins: kBins / C][the slice's keys, when they fit]
+// KEYS: the keys stay in shared memory and a lane's positions, at most 64, as
+// bits of two masks, so that only the first two of the four looks at the keys are
+// at all of them; without, every look reads the weights again.
 template <bool KEYS>
-__global__ void __launch_bounds__(kKeepThreads)
+__global__ void __launch_bounds__(kKeepThreads, 3)
 evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
   extern __shared__ __align__(16) uint32_t dyn[];
   __shared__ KeepShared S;
@@ -92,7 +175,12 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
     if (N0 != N) raise_error(a.err, SD_EBIT_SEQLEN);
     a.new_lens[b] = std::min(N, a.budget);
   }
-  const int j0 = std::min(N, rank * slice_pages * kPage), j1 = std::min(N, j0 + slice_pages * kPage);
+  // equal slices of the sequence, whole pages, at most what the keys have room for
+  const int slice = std::min(slice_pages, ((N + kPage - 1) / kPage + C - 1) / C) * kPage;
+  const int j0 = std::min(N, rank * slice), j1 = std::min(N, j0 + slice);
+  // warp w owns a run of the slice (whole steps of 128 positions, four per lane)
+  const int run = ((j1 - j0 + kKeepWarps - 1) / kKeepWarps + 127) / 128 * 128;
+  const int w0 = std::min(j1, j0 + warp * run), w1 = std::min(j1, w0 + run);
   const int mid0 = a.keep_first, mid1 = N - a.keep_last;         // positions the weights decide about
   const bool all = N <= a.budget;
   const int32_t *pt = a.page_table + (long long)b * sh.max_pages;
@@ -103,147 +191,138 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
     const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.mass + ((long long)page * sh.Hkv + g) * kPage + j % kPage));
     return make_uint4(weight_key(v.x), weight_key(v.y), weight_key(v.z), weight_key(v.w));
   };
-  uint4 *keys4 = reinterpret_cast<uint4 *>(dyn + kBins / C);
-  auto keys_at = [&](int j) -> uint4 { return KEYS ? keys4[(j - j0) / 4] : load4(j); };
+  // of the positions j .. j + 3, as four bits: those of the run that the weights decide about, or that stay anyway
+  auto inner4 = [&](int j) -> uint32_t {
+    if (all) return 0u;
+    uint32_t m = 0u;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) m |= (j + u >= mid0 && j + u < mid1 && j + u < w1) ? 1u << u : 0u;
+    return m;
+  };
+  auto forced4 = [&](int j) -> uint32_t {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) m |= j + u < w1 ? 1u << u : 0u;
+    return m & ~inner4(j);
+  };
+  uint32_t *keys = dyn + kBins / C;
+  uint4 *keys4 = reinterpret_cast<uint4 *>(keys);
   uint32_t tau = 0u;
   int need = a.budget - a.keep_first - a.keep_last;              // in the end: ties of tau that stay
   const bool search = need > 0;
+  const bool some = search && !all;
+  // KEYS: bit 4 i + u of a lane: position w0 + 128 i + 4 lane + u
+  static_assert(kKeepKeysMax / sizeof(uint32_t) / kKeepWarps <= 64 * 32, "a lane's positions are bits of 64");
+  unsigned long long stay = 0ull, cand = 0ull;
   // The number of cluster barriers does not depend on the lengths or the
   // weights: a CTA that read another length (seq_lens written meanwhile) would
   // otherwise leave its cluster waiting.
   if (search && all) {
     for (int k = 0; k < 2 * 3; ++k) cl.sync();
-  } else if (search) {
-    const int widths[3] = {11, 11, 10};
-    uint32_t prefix = 0u, mask = 0u;
-    int shift = 32;
+  }
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int bits = widths[pass], bins = 1 << bits;
-      shift -= bits;
-      for (int x = tid; x < bins; x += kKeepThreads) S.hist[x] = 0u;
-      __syncthreads();
-      const int lo = std::max(j0, mid0), hi = std::min(j1, mid1);  // of the positions the weights decide about
-      uint32_t zeros = 0u;
-      // the first pass loads the slice (each thread comes back to its own positions)
+  for (int pass = 0; pass < (some ? 3 : 0); ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass < 2 ? 2048 : 1024;
+    for (int x = tid; x < bins; x += kKeepThreads) S.hist[x] = 0u;
+    __syncthreads();
+    uint32_t zeros = 0u;
+    auto add = [&](uint32_t k) {
+      if (k == kZeroKey) ++zeros;
+      else atomicAdd(&S.hist[(k >> shift) & (uint32_t)(bins - 1)], 1u);
+    };
+    if (pass == 0 || !KEYS) {
+      const uint32_t mask = pass == 0 ? 0u : ~0u << (shift + (pass == 1 ? 11 : 10));
 #pragma unroll 4
-      for (int j = j0 + 4 * tid; j < j1; j += 4 * kKeepThreads) {
-        uint4 k4;
-        if (pass == 0) {
-          k4 = load4(j);
-          if (KEYS) keys4[(j - j0) / 4] = k4;
-        } else {
-          k4 = keys_at(j);
+      for (int j = w0 + 4 * lane; j < w1; j += 128) {
+        const uint4 k4 = load4(j);
+        const uint32_t m = inner4(j);
+        if (KEYS) {
+          keys4[(j - j0) / 4] = k4;
+          cand |= (unsigned long long)m << ((j - w0) / 128 * 4);
+          stay |= (unsigned long long)forced4(j) << ((j - w0) / 128 * 4);
         }
         const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-        const bool inner = j >= lo && j + 4 <= hi;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if ((m >> u & 1u) && (k[u] & mask) == tau) add(k[u]);
+      }
+    } else if (pass == 1) {                                      // all keys against the first digit
+      unsigned long long next = 0ull;
+      const uint32_t top = tau | ~(~0u << 21);                   // the largest key of that digit
+#pragma unroll 2
+      for (int j = w0 + 4 * lane; j < w1; j += 128) {
+        const uint4 k4 = keys4[(j - j0) / 4];
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        const int at = (j - w0) / 128 * 4;
+        const uint32_t m = (uint32_t)(cand >> at) & 15u;
+        uint32_t above = 0u, same = 0u;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          if (!inner && (j + u < lo || j + u >= hi)) continue;
-          if (k[u] == kZeroKey) ++zeros;
-          else if ((k[u] & mask) == prefix) atomicAdd(&S.hist[(k[u] >> shift) & (bins - 1)], 1u);
+          above |= k[u] > top ? 1u << u : 0u;
+          same |= k[u] >= tau && k[u] <= top ? 1u << u : 0u;
+        }
+        above &= m;
+        same &= m;
+        stay |= (unsigned long long)above << at;
+        next |= (unsigned long long)same << at;
+        if (same) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (same >> u & 1u) add(k[u]);
         }
       }
-      zeros = __reduce_add_sync(kFull, zeros);
-      if (lane == 0 && zeros && (kZeroKey & mask) == prefix) atomicAdd(&S.hist[(kZeroKey >> shift) & (bins - 1)], zeros);
-      cl.sync();
-      // bins of the whole cluster: CTA r sums share r of them (counted from the
-      // highest bin), so that each histogram is read once over the cluster
-      const int share = bins / C;
-      uint32_t tot = 0u;
-      for (int x = tid; x < share; x += kKeepThreads) {
-        const int bin = bins - 1 - (rank * share + x);
-        uint32_t n = 0u;
-        for (int r = 0; r < C; ++r) n += cl.map_shared_rank(S.hist, r)[bin];
-        sums[x] = n;
-        tot += n;
+      cand = next;
+    } else {                                                     // the keys of the first digit against the second
+      const uint32_t top = tau | ~(~0u << 10);
+      for (unsigned long long m = cand; m; m &= m - 1ull) {
+        const int at = __ffsll((long long)m) - 1;
+        const uint32_t k = keys[w0 - j0 + at / 4 * 128 + 4 * lane + at % 4];
+        if (k > top) stay |= 1ull << at;
+        if (k < tau || k > top) cand &= ~(1ull << at);
+        else add(k);
       }
-      tot = __reduce_add_sync(kFull, tot);
-      if (lane == 0) S.wsum[warp] = tot;
-      __syncthreads();
-      if (tid == 0) {
-        uint32_t n = 0u;
-        for (int w = 0; w < kKeepWarps; ++w) n += S.wsum[w];
-        S.share = n;
-        S.digit = S.above = 0u;                                    // the same in every CTA if no bin is found below
-      }
-      cl.sync();                                                 // every histogram read, every share summed
-      // the share that holds the need-th count from the top, then its bin (lane r
-      // reads share r, so that the remote reads are one latency)
-      const uint32_t mine_r = lane < C ? *cl.map_shared_rank(&S.share, lane) : 0u;
-      uint32_t upto = mine_r;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(kFull, upto, o);
-        if (lane >= o) upto += y;
-      }
-      const unsigned enough = __ballot_sync(kFull, upto >= (uint32_t)need);
-      // the shares hold need, unless weights read again have changed under the call
-      const int owner = enough ? __ffs(enough) - 1 : 0;
-      const uint32_t before = __shfl_sync(kFull, upto - mine_r, owner);
-      const uint32_t *sum = cl.map_shared_rank(sums, owner);
-      uint32_t mine[kBins / kKeepThreads];
-      tot = 0u;
-#pragma unroll
-      for (int u = 0; u < kBins / kKeepThreads; ++u) {
-        const int x = tid * (kBins / kKeepThreads) + u;
-        mine[u] = x < share ? sum[x] : 0u;
-        tot += mine[u];
-      }
-      uint32_t incl = tot;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += y;
-      }
-      __syncthreads();                                           // wsum read
-      if (lane == 31) S.wsum[warp] = incl;
-      __syncthreads();
-      uint32_t run = before + incl - tot;
-      for (int w = 0; w < warp; ++w) run += S.wsum[w];
-#pragma unroll
-      for (int u = 0; u < kBins / kKeepThreads; ++u) {
-        if (run < (uint32_t)need && run + mine[u] >= (uint32_t)need) {     // exactly one thread
-          S.digit = (uint32_t)(bins - 1 - (owner * share + tid * (kBins / kKeepThreads) + u));
-          S.above = run;
-        }
-        run += mine[u];
-      }
-      __syncthreads();
-      prefix |= S.digit << shift;
-      mask |= (uint32_t)(bins - 1) << shift;
-      need -= (int)S.above;
     }
-    tau = prefix;
+    zeros = __reduce_add_sync(kFull, zeros);
+    if (lane == 0 && zeros) atomicAdd(&S.hist[(kZeroKey >> shift) & (uint32_t)(bins - 1)], zeros);
+    tau |= search_digit(cl, S, sums, bins, need) << shift;
   }
-  __syncthreads();                                               // every thread's keys
-  const bool some = search && !all;
-  // of the positions j .. j + 3: how many stay outright (low half) and are ties
-  // of tau (high half), and which (bits 0-3 and 4-7 of `bits`)
-  auto count4 = [&](int j, uint32_t &bits, uint4 &k4) -> uint32_t {
-    bits = 0u;
-    if (j >= j1) return 0u;
-    if (some) k4 = keys_at(j);
-    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const bool forced = all || j + u < mid0 || j + u >= mid1;
-      const bool one = forced || (some && k[u] > tau);
-      if (j + u < j1) bits |= one ? 1u << u : ((some && k[u] == tau) ? 16u << u : 0u);
+  if (KEYS && some) {                                            // the remaining keys against all of tau
+    for (unsigned long long m = cand; m; m &= m - 1ull) {
+      const int at = __ffsll((long long)m) - 1;
+      const uint32_t k = keys[w0 - j0 + at / 4 * 128 + 4 * lane + at % 4];
+      if (k > tau) stay |= 1ull << at;
+      if (k != tau) cand &= ~(1ull << at);
     }
-    return __popc(bits & 0xFu) | ((uint32_t)__popc(bits & 0xF0u) << 16);
+  }
+  // of the positions j .. j + 3: which stay outright (bits 0-3) and are ties of tau (bits 4-7)
+  auto bits4 = [&](int j, uint4 &k4) -> uint32_t {
+    if (j >= w1) return 0u;
+    if (KEYS && some) {
+      const int at = (j - w0) / 128 * 4;
+      return ((uint32_t)(stay >> at) & 15u) | ((uint32_t)(cand >> at) & 15u) << 4;
+    }
+    uint32_t bits = forced4(j);
+    if (!KEYS && some) {
+      k4 = load4(j);
+      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w}, m = inner4(j);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (m >> u & 1u) bits |= k[u] > tau ? 1u << u : k[u] == tau ? 16u << u : 0u;
+    }
+    return bits;
   };
-  // warp w owns a run of the slice (whole steps of 128 positions): its counts,
-  // then the places of its positions
-  const int run = ((j1 - j0 + kKeepWarps - 1) / kKeepWarps + 127) / 128 * 128;
-  const int w0 = std::min(j1, j0 + warp * run), w1 = std::min(j1, w0 + run);
+  // the run's counts, then the places of its positions
   uint32_t n1 = 0u, n2 = 0u;
-  for (int j = w0; j < w1; j += 128) {
-    uint32_t bits;
-    uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t n = count4(j + 4 * lane, bits, k4);
-    n1 += n & 0xFFFFu;
-    n2 += n >> 16;
+  if (KEYS && some) {
+    n1 = __popcll(stay);
+    n2 = __popcll(cand);
+  } else {
+    for (int j = w0 + 4 * lane; j < w1; j += 128) {
+      uint4 k4;
+      const uint32_t bits = bits4(j, k4);
+      n1 += __popc(bits & 15u);
+      n2 += __popc(bits >> 4);
+    }
   }
   n1 = __reduce_add_sync(kFull, n1);
   n2 = __reduce_add_sync(kFull, n2);
@@ -271,53 +350,64 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
     eq += S.weq[w];
   }
   cg::cluster_group::arrival_token token = cl.barrier_arrive();  // this CTA has read the others' counts
+  const uint32_t ties = (uint32_t)need;
   int32_t *kept = a.kept + ((long long)b * sh.Hkv + g) * a.budget;
   // new pages of the slots this warp can write in a run of 1024 positions, two per lane and one more
-  const int page0 = (int)(gt + std::min(eq, (uint32_t)need)) / kPage;
+  const int page0 = (int)(gt + std::min(eq, ties)) / kPage;
   auto new_page = [&](int p) {
     return p < sh.max_pages ? __ldg(a.new_page_table + (long long)b * sh.max_pages + p) : -1;
   };
   const bool paged = run <= 32 * 2 * kPage;          // else every slot looks its page up
   const int npage0 = paged ? new_page(page0 + lane) : -1, npage1 = paged ? new_page(page0 + 32 + lane) : -1;
   const int npage2 = paged ? new_page(page0 + 64) : -1;
-  for (int j = w0; j < w1; j += 128) {
-    uint32_t bits;
+  uint2 *stage = reinterpret_cast<uint2 *>(S.hist) + warp * 32;  // position and key of up to 32 rows (no CTA reads the bins now)
+  static_assert(kBins * 4 >= kKeepWarps * 32 * 8, "the stages fit the bins");
+  for (int jw = w0; jw < w1; jw += 128) {
+    const int j = jw + 4 * lane;
     uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t n = count4(j + 4 * lane, bits, k4);
-    if (!some && bits) k4 = load4(j + 4 * lane);                   // the weights move with their rows
-    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+    const uint32_t bits = bits4(j, k4);
+    const uint32_t n = __popc(bits & 15u) | ((uint32_t)__popc(bits >> 4) << 16);
     uint32_t incl = n;                                             // both counts at once: at most 128 each
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t y = __shfl_up_sync(kFull, incl, o);
       if (lane >= o) incl += y;
     }
-    uint32_t g1 = gt + ((incl - n) & 0xFFFFu), e1 = eq + ((incl - n) >> 16);
-    int at[4], page[4];                                            // slot of each kept position, its page
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const bool one = bits & (1u << u), tie = bits & (16u << u);
-      const uint32_t to = g1 + std::min(e1, (uint32_t)need);       // below the budget (unless, as above)
-      at[u] = (one || (tie && e1 < (uint32_t)need)) && to < (uint32_t)a.budget ? (int)to : -1;
-      if (paged) {
-        const int o = at[u] >= 0 ? at[u] / kPage - page0 : 0;
-        const int lo = __shfl_sync(kFull, npage0, o & 31), hi = __shfl_sync(kFull, npage1, o & 31);
-        page[u] = at[u] < 0 ? -1 : o < 32 ? lo : o < 64 ? hi : npage2;
-      } else {
-        page[u] = at[u] >= 0 ? new_page(at[u] / kPage) : -1;
-      }
-      g1 += one;
-      e1 += tie;
+    if (bits) {                                                    // the weights move with their rows
+      if (KEYS && some) k4 = keys4[(j - j0) / 4];
+      else if (KEYS || !some) k4 = load4(j);
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (at[u] >= 0) kept[at[u]] = j + 4 * lane + u;
-      if (page[u] >= 0 && page[u] < sh.num_pages)                  // bad pages are reported by the move
-        a.mass[((long long)page[u] * sh.Hkv + g) * kPage + at[u] % kPage] = key_weight(k[u]);
-    }
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
     const uint32_t tot = __shfl_sync(kFull, incl, 31);
+    const uint32_t first = gt + std::min(eq, ties);
+    uint32_t g1 = gt + ((incl - n) & 0xFFFFu), e1 = eq + ((incl - n) >> 16);
     gt += tot & 0xFFFFu;
     eq += tot >> 16;
+    // rows [from, from + 32) of this step, in order, one per lane: mostly the only ones
+    const int rows = (int)(gt + std::min(eq, ties) - first);
+    for (int from = 0; from < rows; from += 32) {
+      uint32_t gu = g1, eu = e1;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool one = bits & (1u << u), tie = bits & (16u << u);
+        const int at = (int)(gu + std::min(eu, ties) - first) - from;
+        if ((one || (tie && eu < ties)) && at >= 0 && at < 32) stage[at] = make_uint2((uint32_t)(j + u), k[u]);
+        gu += one;
+        eu += tie;
+      }
+      __syncwarp();
+      const uint2 row = stage[lane];
+      const int to = (int)first + from + lane;
+      const int o = from + lane < rows ? to / kPage - page0 : 0;
+      const int p0 = __shfl_sync(kFull, npage0, o & 31), p1 = __shfl_sync(kFull, npage1, o & 31);
+      if (from + lane < rows && to < a.budget) {                   // always below the budget, unless as above
+        const int page = !paged ? new_page(to / kPage) : o < 32 ? p0 : o < 64 ? p1 : npage2;
+        kept[to] = (int)row.x;
+        if (page >= 0 && page < sh.num_pages)                      // bad pages are reported by the move
+          a.mass[((long long)page * sh.Hkv + g) * kPage + to % kPage] = key_weight(row.y);
+      }
+      __syncwarp();                                                // the stage is free again
+    }
   }
   cl.barrier_wait(std::move(token));                             // no CTA leaves while its counts are read
 }
