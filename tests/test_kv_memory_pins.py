@@ -123,6 +123,7 @@ def test_null_contexts_are_refused():
                                             None) == bad
     assert sd.LIB.sparse_decode_select_attend_mass(None, None, None, None, None, None, None, None, 1, None, None, 1,
                                                    None, None, None, 0, None) == bad
+    assert sd.LIB.sparse_decode_mass_clear(None, None, None, 1, None) == bad
     assert sd.LIB.sparse_decode_evict(None, None, None, None, 1, None, 1, 0, 0, None, None, None, None, None, None,
                                       None) == bad
 
