@@ -17,13 +17,14 @@
 //         32 at a time so that a lane writes one.
 //         Bound by latency (two cluster barriers and a scan per pass, about 4 us)
 //         and, with many items, by instructions: 40 registers for three CTAs per
-//         SM (two with 64 registers: 322 against 314 us), and a thread takes four positions at a time (one
-//         page lookup and one 16-byte load; a page's weights of a head are 64
-//         bytes), and the zeros, the weights of rows that nothing attended to
-//         and usually the most common value, are counted in a register instead
-//         of one histogram bin that all lanes would queue at.  The kept weights
-//         themselves are written to the new pages from here: gathered later, 4
-//         bytes would cost 64 of DRAM traffic each.
+//         SM (two with 64 registers: 322 against 314 us), a thread takes four
+//         positions at a time (one page lookup and one 16-byte load; a page's
+//         weights of a head are 64 bytes), and the zeros, the weights of rows
+//         that nothing attended to and usually the most common value, are
+//         counted in a register instead of one histogram bin that all lanes
+//         would queue at.  The kept weights themselves are written to the new
+//         pages from here: gathered later, 4 bytes would cost 64 of DRAM traffic
+//         each.
 //   move  rows are copied 16 bytes per lane, several loads in flight per thread;
 //         the old pages are only read, so any number of CTAs can work on one
 //         sequence.
