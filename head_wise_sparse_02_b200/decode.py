@@ -145,9 +145,10 @@ class DecodeStep:
         return seq, pos, self.page_table[seq, pos // 16].long() * 16 + pos % 16
 
     def make_kv4(self, stream=None):
-        """Build the cache of 4-bit records from the full caches (every cached token)."""
-        self.kv4 = self.sd.kv4_cache()
+        """Build the cache of 4-bit records from the full caches (every cached token).
+        The cache is made on `stream` too: its zeros come before the appends."""
         with _on(stream):
+            self.kv4 = self.sd.kv4_cache()
             _, _, slot = self._positions()
             for at in range(0, slot.numel(), 1 << 16):                  # bounded copies of the rows
                 s = slot[at:at + (1 << 16)]
