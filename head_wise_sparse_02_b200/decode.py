@@ -148,6 +148,7 @@ class DecodeStep:
         """Build the cache of 4-bit records from the full caches (every cached token).
         The cache is made on `stream` too: its zeros come before the appends."""
         with _on(stream):
+            self._replaced(self.kv4)
             self.kv4 = self.sd.kv4_cache()
             _, _, slot = self._positions()
             for at in range(0, slot.numel(), 1 << 16):                  # bounded copies of the rows
@@ -156,10 +157,21 @@ class DecodeStep:
                 v = self.v_cache[s // 16, :, s % 16].contiguous()
                 self.sd.kv4_append(k, v, s.to(torch.int32), self.kv4, stream)
 
-    def keep_mass(self):
-        """Accumulate the attention weights from here on (and size the workspace for it)."""
-        self.mass = self.sd.mass_cache()
-        self.workspace = self.sd.alloc(self.batch, mass=True)[0]
+    @staticmethod
+    def _replaced(*tensors):
+        """Memory that calls on the current stream may still use is not handed out before they end."""
+        for t in tensors:
+            if t is not None:
+                t.record_stream(torch.cuda.current_stream(t.device))
+
+    def keep_mass(self, stream=None):
+        """Accumulate the attention weights from here on (and size the workspace for
+        it).  `stream` is the one that the calls run on: the weights start from zero there."""
+        with _on(stream):
+            self._replaced(self.mass, self.workspace)
+            self.mass = self.sd.mass_cache()
+            self.workspace = torch.empty(self.sd.mass_workspace_size(self.batch), dtype=torch.uint8,
+                                         device=self.sd.device)
 
     def attend_kv4(self, q: torch.Tensor, sel_idx=None, sel_count=None, stream=None) -> torch.Tensor:
         """attend on the 4-bit cache (adding to the accumulated weights, if kept)."""
@@ -212,8 +224,7 @@ class DecodeStep:
             self.sd.evict(self.mass, self.page_table, self.seq_lens, new_page_table, budget, first, last, kept, lens,
                           k_cache=self.k_cache, v_cache=self.v_cache, index_cache=self.index_cache,
                           kv4_cache=self.kv4, stream=stream)
-            for t in (self.page_table, self.seq_lens):                  # read by this stream until here
-                t.record_stream(torch.cuda.current_stream(t.device))
+            self._replaced(self.page_table, self.seq_lens)
         self.page_table, self.seq_lens = new_page_table, lens
         return kept
 

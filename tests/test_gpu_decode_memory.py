@@ -42,3 +42,44 @@ def test_records_made_on_a_side_stream_while_the_current_one_is_busy():
         torch.cuda.synchronize()
         assert st.error_word() == 0 and torch.equal(st.kv4, want)
     st.close()
+
+
+def test_weights_kept_on_a_side_stream_while_the_current_one_is_busy():
+    st, _ = _step()
+    st.make_kv4()
+    st.keep_mass()
+    q = _randn((2, 4, 64), 40)
+    st.select(q)
+    st.attend_kv4(q)
+    torch.cuda.synchronize()
+    want, out = st.mass.clone(), st.out.clone()
+    assert want.any()
+    st.mass.fill_(7.0)                                                 # memory that a new cache may be given again
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(BUSY)
+    st.keep_mass(side)
+    st.attend_kv4(q, stream=side)
+    torch.cuda.synchronize()
+    assert st.error_word() == 0 and torch.equal(st.mass, want) and torch.equal(st.out, out)
+    st.close()
+
+
+def test_memory_replaced_under_a_running_stream_is_not_handed_out():
+    """The workspace and the weights that keep_mass replaces are not given to
+    another tensor while work on the stream that the call was given is pending."""
+    st, _ = _step(lens=(250, 131), maxp=400)
+    st.keep_mass()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    old = [(t.data_ptr(), t.numel() * t.element_size()) for t in (st.workspace, st.mass)]
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    st.keep_mass(side)
+    taken = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in old for _ in range(3)]
+    assert not side.query()                                            # else the test would show nothing
+    for t in taken:
+        for ptr, n in old:
+            assert t.data_ptr() + t.numel() <= ptr or t.data_ptr() >= ptr + n
+    torch.cuda.synchronize()
+    st.close()
