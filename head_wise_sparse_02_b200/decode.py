@@ -11,12 +11,14 @@ import torch
 from .sparse_decode import SparseDecode
 
 
-def _on(stream):
-    """Torch's own operations on the stream that the calls are given (None: the current one)."""
+def _on(stream, device):
+    """Torch's own operations on the stream of `device` that the calls are given
+    (None: the current one; a handle, where 0 is the default stream)."""
     if stream is None:
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream))
+        handle = int(getattr(stream, "cuda_stream", stream))
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
     return torch.cuda.stream(stream)
 
 
@@ -147,7 +149,7 @@ class DecodeStep:
     def make_kv4(self, stream=None):
         """Build the cache of 4-bit records from the full caches (every cached token).
         The cache is made on `stream` too: its zeros come before the appends."""
-        with _on(stream):
+        with _on(stream, self.k_cache.device):
             self._replaced(self.kv4)
             self.kv4 = self.sd.kv4_cache()
             _, _, slot = self._positions()
@@ -167,7 +169,7 @@ class DecodeStep:
     def keep_mass(self, stream=None):
         """Accumulate the attention weights from here on (and size the workspace for
         it).  `stream` is the one that the calls run on: the weights start from zero there."""
-        with _on(stream):
+        with _on(stream, self.k_cache.device):
             self._replaced(self.mass, self.workspace)
             self.mass = self.sd.mass_cache()
             self.workspace = torch.empty(self.sd.mass_workspace_size(self.batch), dtype=torch.uint8,
@@ -217,7 +219,7 @@ class DecodeStep:
         cfg = self.sd.cfg
         first = cfg.get("num_sinks", 0) if keep_first is None else keep_first
         last = cfg.get("window", 0) if keep_last is None else keep_last
-        with _on(stream):
+        with _on(stream, self.k_cache.device):
             kept = torch.full((self.batch, self.k_cache.shape[1], budget), -1, dtype=torch.int32,
                               device=self.k_cache.device)
             lens = torch.empty_like(self.seq_lens)

@@ -83,3 +83,26 @@ def test_memory_replaced_under_a_running_stream_is_not_handed_out():
             assert t.data_ptr() + t.numel() <= ptr or t.data_ptr() >= ptr + n
     torch.cuda.synchronize()
     st.close()
+
+
+def test_streams_given_as_handles():
+    """A raw handle is the stream it names, 0 the default stream, not a fresh one."""
+    from head_wise_sparse_02_b200.decode import _on
+    dev = torch.device("cuda", torch.cuda.current_device())
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(other):
+        for given, handle in ((None, other.cuda_stream), (side, side.cuda_stream), (side.cuda_stream, side.cuda_stream),
+                              (0, 0), (torch.cuda.default_stream(), 0)):
+            with _on(given, dev):
+                assert torch.cuda.current_stream().cuda_stream == handle
+    st, _ = _step(lens=(250, 131))
+    st.make_kv4()
+    torch.cuda.synchronize()
+    want = st.kv4.clone()
+    torch.cuda.synchronize()
+    for given in (0, side.cuda_stream):
+        with torch.cuda.stream(other):
+            st.make_kv4(given)
+        torch.cuda.synchronize()
+        assert st.error_word() == 0 and torch.equal(st.kv4, want)
+    st.close()
