@@ -83,11 +83,14 @@ class DecodeStep:
 
     def step(self, q_pre: torch.Tensor, q: torch.Tensor, new_keys: Optional[torch.Tensor] = None,
              new_slots: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-        """One decode step: index the appended tokens, then select and attend."""
+        """One decode step: index the appended tokens (whose accumulated weights, if
+        kept, start from zero), then select and attend (adding to them)."""
         if new_keys is not None:
             self.sd.index_keys(new_keys, new_slots, self.index_cache, stream)
             if self.mass is not None:
                 self.sd.mass_clear(self.mass, new_slots, stream)
+        if self.mass is not None:
+            return self.select_attend_mass(q_pre, q, stream)
         return self.select_attend(q_pre, q, stream)
 
     # ---- split layout: paged caches of the retrieval groups, compacted local caches
@@ -167,8 +170,10 @@ class DecodeStep:
                 t.record_stream(torch.cuda.current_stream(t.device))
 
     def keep_mass(self, stream=None):
-        """Accumulate the attention weights from here on (and size the workspace for
-        it).  `stream` is the one that the calls run on: the weights start from zero there."""
+        """Accumulate the attention weights of step, step_kv4, select_attend_mass,
+        attend_kv4 and select_attend_kv4 from here on (and size the workspace for it);
+        the other attention calls leave them as they are.  `stream` is the one that the
+        calls run on: the weights start from zero there."""
         with _on(stream, self.k_cache.device):
             self._replaced(self.mass, self.workspace)
             self.mass = self.sd.mass_cache()

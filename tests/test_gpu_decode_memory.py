@@ -106,3 +106,85 @@ def test_streams_given_as_handles():
         torch.cuda.synchronize()
         assert st.error_word() == 0 and torch.equal(st.kv4, want)
     st.close()
+
+
+@pytest.mark.parametrize("d,G,retr", [(64, 4, [1] * 4 + [0] * 4), (128, 2, [1, 0, 1, 1])])
+def test_bf16_decode_loop_accumulates_and_evicts(d, G, retr):
+    """Eleven steps on bf16 caches with an eviction in the middle, against a float64
+    model on the same sets: outputs, accumulated weights, kept positions.
+    Tolerances as in test_gpu_kv4, with 2^-24 of a weight's sum per addition."""
+    B, Hkv, window, sinks, budget = 2, 2, 16, 2, 80
+    st, tables = _step(Hkv=Hkv, G=G, d=d, lens=(140, 50), maxp=12, seed=11, retr=retr, window=window, sinks=sinks, frac=0.25,
+                       tables=2)
+    _, _, slot = st._positions()
+    st.build_index(slot.to(torch.int32), st.k_cache[slot // 16, :, slot % 16].contiguous())
+    st.keep_mass()
+    model = {}
+    for b, n in enumerate(st.seq_lens.tolist()):
+        pg = st.page_table[b].long().repeat_interleave(16)[:n]
+        off = torch.arange(n, device="cuda") % 16
+        for g in range(Hkv):
+            model[b, g] = [x[pg, g, off].double().cpu().numpy() for x in (st.k_cache, st.v_cache)] + [np.zeros(n), np.zeros(n)]
+    for i in range(11):
+        new_k, new_v, q = _randn((B, Hkv, d), 100 + i), _randn((B, Hkv, d), 200 + i), _randn((B, G * Hkv, d), 300 + i)
+        n = st.seq_lens.tolist()
+        slots = torch.tensor([int(st.page_table[b, n[b] // 16]) * 16 + n[b] % 16 for b in range(B)], dtype=torch.int32,
+                             device="cuda")
+        sl = slots.long()
+        st.k_cache[sl // 16, :, sl % 16], st.v_cache[sl // 16, :, sl % 16] = new_k, new_v
+        st.mass[sl // 16, :, sl % 16] = 1e6                            # what an earlier token left
+        st.seq_lens.add_(1)
+        out = st.step(q, q, new_k, slots).cpu().numpy()
+        assert st.error_word() == 0
+        cnt, idx, qn = st.sel_count.cpu().numpy(), st.sel_idx.cpu().numpy(), q.double().cpu().numpy()
+        for b in range(B):
+            N = n[b] + 1
+            for g in range(Hkv):
+                K, V, m, tol = model[b, g]
+                K, V = np.vstack([K, new_k[b, g].double().cpu().numpy()]), np.vstack([V, new_v[b, g].double().cpu().numpy()])
+                m, tol = np.append(m, 0.0), np.append(tol, 0.0)
+                for h in range(g * G, (g + 1) * G):
+                    if retr[h]:
+                        r = sum(retr[:h])
+                        s = idx[b, r, :cnt[b, r]]
+                        assert s.size == max(1, int(0.25 * N))
+                    else:
+                        s = np.concatenate([np.arange(sinks), np.arange(max(sinks, N - window), N)])
+                    w = O.set_weights(qn[b, h], K[s], d ** -0.5)
+                    A = LOG2E * d ** -0.5 * (np.abs(K[s]) @ np.abs(qn[b, h])).max()
+                    assert np.abs(out[b, h] - w @ V[s]).max() <= (4.2e-6 * A + 3e-5) * np.abs(V[s]).max(), (i, b, h)
+                    m[s] += w
+                    tol[s] += (4.2e-6 * A + 1e-6) * w + 2.0 ** -24 * m[s]
+                model[b, g] = [K, V, m, tol]
+                got = _weights(st, b, g, N)
+                assert (np.abs(got - m) <= tol).all(), (i, b, g)
+        if i == 5:
+            lens = st.seq_lens.tolist()
+            old = {(b, g): _weights(st, b, g, lens[b]) for b in range(B) for g in range(Hkv)}
+            kept = st.evict(tables[1], budget).cpu().numpy()
+            assert st.error_word() == 0 and st.seq_lens.tolist() == [min(x, budget) for x in lens]
+            for (b, g), m in old.items():
+                exp = O.evict_positions(m, lens[b], budget, sinks, window)
+                assert kept[b, g, :len(exp)].tolist() == exp and (kept[b, g, len(exp):] == -1).all()
+                model[b, g] = [x[exp] for x in model[b, g]]
+    st.close()
+
+
+def test_calls_that_do_not_accumulate_leave_the_weights():
+    st, _ = _step()
+    q = _randn((2, 4, 64), 40)
+    plain = st.step(q, q).clone()                                      # no weights kept: the plain call
+    assert torch.equal(plain, st.select_attend(q, q))
+    st.keep_mass()
+    st.select_attend(q, q)
+    st.attend(q)
+    assert not st.mass.any()
+    st.step(q, q)                                                      # no new token: still accumulates
+    assert abs(float(st.mass.double().sum()) - 8) <= 1e-4              # eight heads with a set, weights summing to one
+    assert st.error_word() == 0
+    st.close()
+
+
+def _weights(st, b, g, n):
+    pg = st.page_table[b].long().repeat_interleave(16)[:n]
+    return st.mass[pg, g, torch.arange(n, device="cuda") % 16].double().cpu().numpy()
