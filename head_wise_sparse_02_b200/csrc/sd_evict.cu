@@ -185,10 +185,14 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
   const int mid0 = a.keep_first, mid1 = N - a.keep_last;         // positions the weights decide about
   const bool all = N <= a.budget;
   const int32_t *pt = a.page_table + (long long)b * sh.max_pages;
-  // keys of the positions j .. j + 3 (j a multiple of four: one page)
+  // keys of the positions j .. j + 3 (j a multiple of four: one page); of a bad
+  // page 0, below every number's
   auto load4 = [&](int j) -> uint4 {
     const int page = __ldg(pt + j / kPage);
-    if (page < 0 || page >= sh.num_pages) return make_uint4(0u, 0u, 0u, 0u);   // reported by the move
+    if (page < 0 || page >= sh.num_pages) {
+      raise_error(a.err, SD_EBIT_PAGE);
+      return make_uint4(0u, 0u, 0u, 0u);
+    }
     const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.mass + ((long long)page * sh.Hkv + g) * kPage + j % kPage));
     return make_uint4(weight_key(v.x), weight_key(v.y), weight_key(v.z), weight_key(v.w));
   };
@@ -404,8 +408,12 @@ evict_keep_kernel(const EvictArgs a, const Shape sh, int slice_pages) {
       if (from + lane < rows && to < a.budget) {                   // always below the budget, unless as above
         const int page = !paged ? new_page(to / kPage) : o < 32 ? p0 : o < 64 ? p1 : npage2;
         kept[to] = (int)row.x;
-        if (page >= 0 && page < sh.num_pages)                      // bad pages are reported by the move
-          a.mass[((long long)page * sh.Hkv + g) * kPage + to % kPage] = key_weight(row.y);
+        bool ok = page >= 0 && page < sh.num_pages;                // else reported by the move, which skips the row too
+        if (row.y == 0u) {                                         // a NaN, or a row of a bad page: skipped
+          const int from = __ldg(pt + row.x / kPage);
+          ok = ok && from >= 0 && from < sh.num_pages;
+        }
+        if (ok) a.mass[((long long)page * sh.Hkv + g) * kPage + to % kPage] = key_weight(row.y);
       }
       __syncwarp();                                                // the stage is free again
     }

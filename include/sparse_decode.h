@@ -637,7 +637,9 @@ SD_API sd_status sparse_decode_mass_clear(sd_ctx *ctx, float *mass, const int32_
  *                   keep_first + keep_last <= budget.
  *
  * No workspace.  A page id outside the pool sets SD_EBIT_PAGE and its rows are
- * skipped.
+ * skipped: their weights count below every number, and where such a row is kept
+ * all the same its new slot is left as it was, in the caches and in mass.  (With
+ * keep_first + keep_last == budget the pages of the other positions are not read.)
  */
 SD_API sd_status sparse_decode_evict(sd_ctx *ctx, float *mass, const int32_t *page_table, const int32_t *seq_lens,
                               int batch, const int32_t *new_page_table, int budget, int keep_first, int keep_last,

@@ -1,0 +1,70 @@
+"""Edges of the 4-bit attention, the weight-keeping attention and the eviction
+(through the C ABI): rows that some heads of a group leave out, bad pages met
+alone, workspaces of the plain calls, and results that do not depend on what ran
+before."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_evict import Pool
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ eviction past a bad page
+
+@pytest.mark.parametrize("lens,budget,first,last,maxp,bad", [
+    ([200, 90], 50, 4, 10, None, 5),                  # a page that the weights decide about
+    ([200, 90], 50, 4, 10, None, 0),                  # the first positions, which stay anyway
+    ([40, 90], 64, 0, 0, None, 1),                    # everything stays
+    ([200, 90], 14, 4, 10, None, 0),                  # the weights decide about nothing
+    ([5000, 300], 1200, 4, 50, 20000, 0),             # weights read again each time
+    ([5000, 300], 1200, 4, 50, 20000, 100),
+])
+@pytest.mark.parametrize("page", ["past the pool", "negative"])
+def test_one_bad_source_page_is_reported_and_its_rows_skipped(lens, budget, first, last, maxp, bad, page):
+    from head_wise_sparse_02_b200.sparse_decode import SD_EBIT_PAGE
+    p = Pool(lens, budget, 2, 64, "plain", seed=len(lens) + budget + bad, maxp=maxp)
+    p.mass += 1.0
+    good = p.table.copy()
+    p.table[0, bad] = p.mass.shape[0] if page == "past the pool" else -1
+    p.run(first, last)
+    torch.cuda.synchronize()
+    assert p.sd.error_word() == SD_EBIT_PAGE
+    assert p.new_lens.tolist() == [min(n, budget) for n in lens]
+    kept = p.kept.cpu().numpy()
+    want = {k: v.clone() for k, v in p.before.items()}
+    for b, n in enumerate(lens):
+        for g in range(2):
+            j = kept[b, g, :min(n, budget)].astype(np.int64)
+            assert (np.diff(j) > 0).all() and 0 <= j[0] and j[-1] < n
+            i = np.arange(j.size)
+            if b == 0:
+                ok = j // 16 != bad
+                assert n <= budget or not ok.all() or bad != 0          # the forced ones stay listed
+                j, i = j[ok], i[ok]
+            src = tuple(torch.from_numpy(x).cuda() for x in (good[b, j // 16].astype(np.int64), j % 16))
+            dst = tuple(torch.from_numpy(x).cuda() for x in (p.new_table[b, i // 16].astype(np.int64), i % 16))
+            for k in want:
+                want[k][dst[0], g, dst[1]] = p.before[k][src[0], g, src[1]]
+    assert torch.isfinite(p.mass).all()
+    for k, v in (*p.caches.items(), ("mass", p.mass)):
+        assert torch.equal(v.view(torch.uint8), want[k].view(torch.uint8)), k
+    p.sd.close()
+
+
+def test_weights_of_every_nan_move_as_they_are():
+    """A NaN of all bits set has the key that rows of bad pages get: it is moved all the same."""
+    p = Pool([40, 90], 64, 1, 64, "plain", seed=3)
+    bits = p.mass.view(torch.int32)
+    for b, j, word in ((0, 3, -1), (0, 39, -2), (1, 0, -1), (1, 88, 0x7FC00000)):
+        bits[int(p.table[b, j // 16]), 0, j % 16] = word
+    p.run(4, 10)
+    torch.cuda.synchronize()
+    assert p.sd.error_word() == 0
+    for b, n in ((0, 40), (1, 64)):
+        for i, j in enumerate(p.kept[b, 0, :n].tolist()):
+            assert int(bits[int(p.new_table[b, i // 16]), 0, i % 16]) == \
+                int(p.before["mass"].view(torch.int32)[int(p.table[b, j // 16]), 0, j % 16])
+    p.sd.close()
