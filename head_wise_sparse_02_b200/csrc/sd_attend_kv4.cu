@@ -20,10 +20,13 @@
 // The other operand takes powers of two that keep it in f16's range:
 //   q  times 2^k, its largest element in [2^14, 2^15): exact down to 2^-29 of
 //      the largest, and off by at most 2^-40 of it below;
-//   p s  times 2^-R_g, R_g per group such that the largest s of the first tile
-//      lies in [2^10, 2^11), moved only when a larger s comes along; p s is split
-//      into f16 hi + lo terms, together within 2^-22 of it (or 2^-34 of the
-//      largest), so that weights keep nearly float32 accuracy.
+//   p s  times 2^-R_g, R_g per group and head such that the largest s of the
+//      head's rows in its first tile lies in [2^10, 2^11), moved only when a larger
+//      s of one of its rows comes along (with one R_g for all heads, rows that a
+//      head leaves out would set its precision: values 2^60 times its own left
+//      nothing of its codes); p s is split into f16 hi + lo terms, together within
+//      2^-22 of it (or 2^-34 of the head's largest), so that weights keep nearly
+//      float32 accuracy.
 // The softmax reference of a head also moves only when a logit exceeds it by
 // 2^4, so most tiles need no exchange for the maximum and no rescaling.
 //
@@ -271,14 +274,14 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
   __syncthreads();
   float m[HB], l[HB], o[HB][NG][2][4];
   float2 olo[HB][NG];                                // two partial sums each
-  uint32_t nf[NG / 2], thr[NG / 2];                  // bf16 pairs: 2^-R_g, and the largest s it serves
-#pragma unroll
-  for (int w = 0; w < NG / 2; ++w) {
-    nf[w] = 0x3F803F80u;
-    thr[w] = 0u;
-  }
+  uint32_t nf[HB][NG / 2], thr[HB][NG / 2];          // of the lane's heads, bf16 pairs: 2^-R_g, and the largest s it serves
 #pragma unroll
   for (int hb = 0; hb < HB; ++hb) {
+#pragma unroll
+    for (int w = 0; w < NG / 2; ++w) {
+      nf[hb][w] = 0x3F803F80u;
+      thr[hb][w] = 0u;
+    }
     m[hb] = -INFINITY;
     l[hb] = 0.0f;
 #pragma unroll
@@ -433,13 +436,8 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
         }
       }
     bool over = false;
-    uint32_t smax[NG / 2];
-#pragma unroll
-    for (int w = 0; w < NG / 2; ++w) {
-      smax[w] = max_bf16x2(vs[0][0][w], vs[0][1][w]);
-      if constexpr (!PACK) smax[w] = max_bf16x2(smax[w], max_bf16x2(vs[NJ - 1][0][w], vs[NJ - 1][1][w]));
-      over |= any_gt_bf16x2(smax[w], thr[w]);
-    }
+    uint32_t vh[HB][NJ][2][NG / 2];                  // of each head: the scales of its rows, 0 of the others'
+    uint32_t smax[HB][NG / 2];
     float top[HB];                                   // the lane's largest logit
 #pragma unroll
     for (int hb = 0; hb < HB; ++hb) {
@@ -451,6 +449,11 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
         const uint32_t mk = *reinterpret_cast<const uint32_t *>(wmask + (q % kRing4) * kTileRows + 4 * tq + 2 * j);
         x[hb][jj].x = (mk & bit) ? x[hb][jj].x * qsc[hb] : -INFINITY;
         x[hb][jj].y = (mk & (bit << 16)) ? x[hb][jj].y * qsc[hb] : -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NG / 2; ++w) {
+          vh[hb][jj][0][w] = (mk & bit) ? vs[jj][0][w] : 0u;
+          vh[hb][jj][1][w] = (mk & (bit << 16)) ? vs[jj][1][w] : 0u;
+        }
         top[hb] = fmaxf(top[hb], fmaxf(x[hb][jj].x, x[hb][jj].y));
         if constexpr (MASS)
           if (hd + 8 * hb < nh)
@@ -458,34 +461,40 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
                                         4 * tq + 2 * j) = x[hb][jj];
       }
       over |= top[hb] > m[hb] + kLazy;
+#pragma unroll
+      for (int w = 0; w < NG / 2; ++w) {
+        smax[hb][w] = max_bf16x2(vh[hb][0][0][w], vh[hb][0][1][w]);
+        if constexpr (!PACK) smax[hb][w] = max_bf16x2(smax[hb][w], max_bf16x2(vh[hb][NJ - 1][0][w], vh[hb][NJ - 1][1][w]));
+        over |= any_gt_bf16x2(smax[hb][w], thr[hb][w]);
+      }
     }
     if (__any_sync(kFull, over)) {
       // move the references: of every head to its maximum so far, of a group's
       // scales where one outgrew it
-      float rf[NG];                                  // 2^(old R - new R)
-#pragma unroll
-      for (int w = 0; w < NG / 2; ++w) {
-        uint32_t top_s = max_bf16x2(smax[w], __shfl_xor_sync(kFull, smax[w], 1));
-        top_s = max_bf16x2(top_s, __shfl_xor_sync(kFull, top_s, 2));
-        if constexpr (PACK) top_s = max_bf16x2(top_s, __shfl_xor_sync(kFull, top_s, 16));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float sv = i ? bf16_hi(top_s) : bf16_lo(top_s), lim = i ? bf16_hi(thr[w]) : bf16_lo(thr[w]);
-          const float old = i ? bf16_hi(nf[w]) : bf16_lo(nf[w]);
-          rf[2 * w + i] = 1.0f;
-          if (sv > lim) {
-            const int e = std::min(110, std::max(-110, exponent_of(sv)));
-            const float nn = pow2i(kScaleTop - e), nl = pow2i(e + 1);   // s 2^-R in [2^10, 2^11); serves up to 2^(e + 1)
-            rf[2 * w + i] = lim > 0.0f ? nn / old : 1.0f;     // powers of two: exact
-            const uint32_t keep = i ? 0x0000FFFFu : 0xFFFF0000u;
-            const uint32_t nb = __float_as_uint(nn) >> 16, lb = __float_as_uint(nl) >> 16;
-            nf[w] = (nf[w] & keep) | (i ? nb << 16 : nb);
-            thr[w] = (thr[w] & keep) | (i ? lb << 16 : lb);
-          }
-        }
-      }
 #pragma unroll
       for (int hb = 0; hb < HB; ++hb) {
+        float rf[NG];                                // 2^(old R - new R)
+#pragma unroll
+        for (int w = 0; w < NG / 2; ++w) {
+          uint32_t top_s = max_bf16x2(smax[hb][w], __shfl_xor_sync(kFull, smax[hb][w], 1));
+          top_s = max_bf16x2(top_s, __shfl_xor_sync(kFull, top_s, 2));
+          if constexpr (PACK) top_s = max_bf16x2(top_s, __shfl_xor_sync(kFull, top_s, 16));   // the other half tile
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float sv = i ? bf16_hi(top_s) : bf16_lo(top_s), lim = i ? bf16_hi(thr[hb][w]) : bf16_lo(thr[hb][w]);
+            const float old = i ? bf16_hi(nf[hb][w]) : bf16_lo(nf[hb][w]);
+            rf[2 * w + i] = 1.0f;
+            if (sv > lim) {
+              const int e = std::min(110, std::max(-110, exponent_of(sv)));
+              const float nn = pow2i(kScaleTop - e), nl = pow2i(e + 1);   // s 2^-R in [2^10, 2^11); serves up to 2^(e + 1)
+              rf[2 * w + i] = lim > 0.0f ? nn / old : 1.0f;     // powers of two: exact
+              const uint32_t keep = i ? 0x0000FFFFu : 0xFFFF0000u;
+              const uint32_t nb = __float_as_uint(nn) >> 16, lb = __float_as_uint(nl) >> 16;
+              nf[hb][w] = (nf[hb][w] & keep) | (i ? nb << 16 : nb);
+              thr[hb][w] = (thr[hb][w] & keep) | (i ? lb << 16 : lb);
+            }
+          }
+        }
         float tm = fmaxf(top[hb], __shfl_xor_sync(kFull, top[hb], 1));
         tm = fmaxf(tm, __shfl_xor_sync(kFull, tm, 2));
         if constexpr (PACK) tm = fmaxf(tm, __shfl_xor_sync(kFull, tm, 16));   // the other half tile
@@ -493,17 +502,17 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
         const float al = mn == m[hb] ? 1.0f : fast_exp2(m[hb] - mn);   // 0 from -inf
         m[hb] = mn;
         l[hb] *= al;
-        const float a0 = __shfl_sync(kFull, al, 8 * tq), a1 = __shfl_sync(kFull, al, 8 * tq + 4);   // columns 2 tq, 2 tq + 1
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           olo[hb][g] = mul2(olo[hb][g], make_float2(al, al));
-          const float r = rf[g];
+          const float f = al * rf[g];
+          const float f0 = __shfl_sync(kFull, f, 8 * tq), f1 = __shfl_sync(kFull, f, 8 * tq + 4);   // columns 2 tq, 2 tq + 1
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
-            o[hb][g][mt][0] *= a0 * r;
-            o[hb][g][mt][1] *= a1 * r;
-            o[hb][g][mt][2] *= a0 * r;
-            o[hb][g][mt][3] *= a1 * r;
+            o[hb][g][mt][0] *= f0;
+            o[hb][g][mt][1] *= f1;
+            o[hb][g][mt][2] *= f0;
+            o[hb][g][mt][3] *= f1;
           }
         }
       }
@@ -535,11 +544,13 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
       }
 #pragma unroll
     for (int w = 0; w < NG / 2; ++w) {
-      uint32_t vn[NJ][2];
+      uint32_t vn[HB][NJ][2];
 #pragma unroll
-      for (int jj = 0; jj < NJ; ++jj)
+      for (int hb = 0; hb < HB; ++hb)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) vn[jj][e] = mul_bf16x2(vs[jj][e][w], nf[w]);   // times 2^-R: exact
+        for (int jj = 0; jj < NJ; ++jj)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) vn[hb][jj][e] = mul_bf16x2(vh[hb][jj][e][w], nf[hb][w]);   // times 2^-R: exact
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int g = 2 * w + i;
@@ -553,9 +564,9 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
           uint32_t bh[2], bl[2];
 #pragma unroll
           for (int jj = 0; jj < NJ; ++jj) {
-            const float2 ps = mul2(x[hb][jj], halves(vn[jj][0], vn[jj][1], i));
+            const float2 ps = mul2(x[hb][jj], halves(vn[hb][jj][0], vn[hb][jj][1], i));
             // lo and 8 s nearly cancel: joined first, so that the sum keeps its precision
-            const float2 mid = fma2(halves(vs[jj][0][w], vs[jj][1][w], i), make_float2(8.0f, 8.0f),
+            const float2 mid = fma2(halves(vh[hb][jj][0][w], vh[hb][jj][1][w], i), make_float2(8.0f, 8.0f),
                                     halves(vl[jj][0][w], vl[jj][1][w], i));
             olo[hb][g] = fma2(x[hb][jj], mid, olo[hb][g]);
             bh[jj] = pack_f16(ps.x, ps.y);
@@ -626,7 +637,8 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const float z0 = __shfl_sync(kFull, olo[hb][g].x, 8 * tq), z1 = __shfl_sync(kFull, olo[hb][g].x, 8 * tq + 4);
-      const float un = 1.0f / ((g & 1) ? bf16_hi(nf[g / 2]) : bf16_lo(nf[g / 2]));   // 2^R: exact
+      const float un = 1.0f / ((g & 1) ? bf16_hi(nf[hb][g / 2]) : bf16_lo(nf[hb][g / 2]));   // 2^R: exact
+      const float un0 = __shfl_sync(kFull, un, 8 * tq), un1 = __shfl_sync(kFull, un, 8 * tq + 4);
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         float v[4];
@@ -637,8 +649,8 @@ attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const Att
         }
         if (!PACK || tq < 2) {
           float *d0 = cacc + (warp * GR + 8 * hb + 2 * tq) * D + g * kKv4Group + 4 * gq + 2 * mt;
-          *reinterpret_cast<float2 *>(d0) = make_float2(fmaf(v[0], un, z0), fmaf(v[2], un, z0));
-          *reinterpret_cast<float2 *>(d0 + D) = make_float2(fmaf(v[1], un, z1), fmaf(v[3], un, z1));
+          *reinterpret_cast<float2 *>(d0) = make_float2(fmaf(v[0], un0, z0), fmaf(v[2], un0, z0));
+          *reinterpret_cast<float2 *>(d0 + D) = make_float2(fmaf(v[1], un1, z1), fmaf(v[3], un1, z1));
         }
       }
     }

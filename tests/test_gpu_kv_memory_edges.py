@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from tests.test_gpu_evict import Pool
+from tests.test_gpu_kv4 import Case
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +69,24 @@ def test_weights_of_every_nan_move_as_they_are():
             assert int(bits[int(p.new_table[b, i // 16]), 0, i % 16]) == \
                 int(p.before["mass"].view(torch.int32)[int(p.table[b, j // 16]), 0, j % 16])
     p.sd.close()
+
+
+# ------------------------------------------------------------------ values of rows that a head leaves out
+
+@pytest.mark.parametrize("power", [24, 60, -60])
+@pytest.mark.parametrize("d,G", [(128, 2), (128, 4), (64, 4), (128, 8), (64, 8), (128, 16), (64, 16)])
+def test_values_a_head_leaves_out_do_not_cost_it_precision(d, G, power):
+    """Every fifth row's values are 2^power times the others'.  Heads 0 and G / 2
+    leave those rows out, the last head takes them all, the others are mixed: the
+    tolerance of each is that of its own set (as in test_gpu_kv4)."""
+    n = 700
+    c = Case([n, 90], G, 1, d, [1] * G, 0, 0, seed=G + d, vscale=lambda p: torch.where(p % 5 == 0, 2.0 ** power, 1.0))
+    for b, N in enumerate((n, 90)):
+        row = np.arange(c.start[b], c.start[b] + N)                    # vscale went by the token's number
+        for h, s in ((0, np.flatnonzero(row % 5 != 0)), (G // 2, np.flatnonzero(row % 5 != 0)[::2]), (G - 1, np.arange(N))):
+            c.sets[b, h] = s.astype(np.int64)
+            c.sel_idx[b, h, :s.size] = torch.from_numpy(s).to(torch.int32).cuda()
+            c.sel_count[b, h] = s.size
+    c.run("kv4", True)
+    c.check("kv4", True, f"2^{power}")
+    c.sd.close()
