@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <map>
 #include <mutex>
+#include <tuple>
 
 #include "sd_internal.cuh"
 
@@ -355,15 +356,16 @@ cudaError_t set_smem(K kern, size_t bytes) {
   return e;
 }
 
-// resident CTAs of a kernel on this device (cached)
+// resident CTAs of a kernel on this device (cached; the shared memory goes by the
+// context, and the shares and with them the order of the sums by this number)
 template <typename K>
 int resident_ctas(K kern, int threads, size_t smem) {
   static std::mutex mu;
-  static std::map<std::pair<const void *, int>, int> cache;
+  static std::map<std::tuple<const void *, int, int, size_t>, int> cache;
   int dev = 0;
   cudaGetDevice(&dev);
   std::lock_guard<std::mutex> lk(mu);
-  const auto key = std::make_pair((const void *)kern, dev);
+  const auto key = std::make_tuple((const void *)kern, dev, threads, smem);
   auto it = cache.find(key);
   if (it != cache.end()) return it->second;
   int occ = 0, sms = 0;

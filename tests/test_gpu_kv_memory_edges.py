@@ -3,6 +3,10 @@
 alone, workspaces of the plain calls, and results that do not depend on what ran
 before."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -11,6 +15,8 @@ from tests.test_gpu_evict import Pool
 from tests.test_gpu_kv4 import Case
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 # ------------------------------------------------------------------ eviction past a bad page
@@ -90,3 +96,48 @@ def test_values_a_head_leaves_out_do_not_cost_it_precision(d, G, power):
     c.run("kv4", True)
     c.check("kv4", True, f"2^{power}")
     c.sd.close()
+
+
+# ------------------------------------------------------------------ the same bits whatever ran before
+
+ORDER = """
+import hashlib, sys, torch
+from tests.test_gpu_kv4 import _context, _randn
+n, d = 90000, 64
+k, v, q = _randn((n // 16, 1, 16, d), 1), _randn((n // 16, 1, 16, d), 2), _randn((1, 1, d), 3)
+lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+kv4 = None
+for maxp in map(int, sys.argv[1].split(",")):
+    sd = _context([0], 1, d, n // 16, maxp, 1, window=n)
+    table = torch.zeros((1, maxp), dtype=torch.int32, device="cuda")
+    table[0, :n // 16] = torch.arange(n // 16, device="cuda")
+    if kv4 is None:
+        kv4 = sd.kv4_cache()
+        rows = [x.transpose(1, 2).reshape(n, 1, d).contiguous() for x in (k, v)]
+        sd.kv4_append(*rows, torch.arange(n, dtype=torch.int32, device="cuda"), kv4)
+    ws, mass, got = sd.alloc(1, mass=True)[0], sd.mass_cache(), []
+    for form in ("plain", "mass", "kv4", "kv4 mass"):
+        out = torch.full((1, 1, d), float("nan"), device="cuda")
+        args = (table, lens, None, None, out)
+        if form == "plain":
+            sd.attend(q, k, v, *args, ws)
+        elif form == "mass":
+            sd.attend_mass(q, k, v, *args, mass, ws)
+        else:
+            sd.attend_kv4(q, kv4, *args, ws, mass=mass if form == "kv4 mass" else None)
+        got.append(out.cpu().numpy().tobytes())
+    assert sd.error_word() == 0
+print("bits", *(hashlib.sha256(x).hexdigest() for x in got))
+"""
+
+
+def test_results_do_not_depend_on_the_context_that_ran_first():
+    """A page table of 2^21 entries needs kilobytes of span list per CTA, which
+    leaves room for fewer of them on an SM than a short one does; which context a
+    process used first must not show in the other's sums."""
+    def bits(order):
+        r = subprocess.run([sys.executable, "-c", ORDER, order], cwd=ROOT, capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0, r.stderr[-3000:]
+        return [line for line in r.stdout.splitlines() if line.startswith("bits")][0]
+    assert bits(f"{1 << 21}") == bits(f"6000,{1 << 21}")
+    assert bits("6000") == bits(f"{1 << 21},6000")
