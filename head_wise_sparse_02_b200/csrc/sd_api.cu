@@ -60,8 +60,10 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 long long local_rows(const sd_ctx *ctx) { return (long long)ctx->cfg.num_sinks + ctx->cfg.window; }
 
 struct WsLayout {
-  size_t scores_off, flags_off, scores_bytes, stream_off, stream_bytes, att_off, total;
-  size_t total_mass;                  // for the calls that accumulate weights
+  size_t scores_off, flags_off, scores_bytes, stream_off, stream_bytes, att_off;
+  // for the bf16 calls, for those on 4-bit records (and so for either: what the
+  // size query reports), for those that accumulate weights
+  size_t plain, total, total_mass;
 };
 
 WsLayout layout(const sd_ctx *ctx, int batch) {
@@ -73,7 +75,8 @@ WsLayout layout(const sd_ctx *ctx, int batch) {
   w.stream_off = w.scores_off + w.scores_bytes;
   w.stream_bytes = align256(sd::stream_workspace_bytes(ctx->sh, ctx->tb, batch, ctx->cfg.mode));
   w.att_off = w.stream_off + w.stream_bytes;
-  w.total = align256(w.att_off + sd::attend_workspace_bytes(ctx->sh, ctx->tb, batch));
+  w.plain = align256(w.att_off + sd::attend_workspace_bytes(ctx->sh, ctx->tb, batch, false));
+  w.total = align256(w.att_off + sd::attend_workspace_bytes(ctx->sh, ctx->tb, batch, true));
   w.total_mass = align256(w.att_off + sd::attend_mass_workspace_bytes(ctx->sh, ctx->tb, batch, local_rows(ctx)));
   return w;
 }
@@ -135,7 +138,7 @@ sd_status attend_impl(sd_ctx *ctx, const void *q_pre, const void *q, const void 
     }
   }
   const WsLayout w = layout(ctx, batch);
-  if (!workspace || ws_bytes < (form.mass ? w.total_mass : w.total))
+  if (!workspace || ws_bytes < (form.mass ? w.total_mass : form.kv4 ? w.total : w.plain))
     return fail(ctx, SD_ERR_WORKSPACE, "workspace too small");
   DeviceGuard dg(ctx->device);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -352,7 +355,7 @@ sd_status sparse_decode_select(sd_ctx *ctx, const void *q_pre, const void *index
     if (sel_stride < need_stride)
       return fail(ctx, SD_ERR_INVALID_ARG, "sel_stride smaller than the largest possible set");
     const WsLayout w = layout(ctx, batch);
-    if (!workspace || ws_bytes < w.total) return fail(ctx, SD_ERR_WORKSPACE, "workspace too small");
+    if (!workspace || ws_bytes < w.plain) return fail(ctx, SD_ERR_WORKSPACE, "workspace too small");
     DeviceGuard dg(ctx->device);
     sd::SelectArgs a{};
     a.q_pre = static_cast<const uint16_t *>(q_pre);
@@ -395,7 +398,7 @@ sd_status sparse_decode_select_exact(sd_ctx *ctx, const void *q, const void *k_c
     if (sel_stride < need_stride)
       return fail(ctx, SD_ERR_INVALID_ARG, "sel_stride smaller than the largest possible set");
     const WsLayout w = layout(ctx, batch);
-    if (!workspace || ws_bytes < w.total) return fail(ctx, SD_ERR_WORKSPACE, "workspace too small");
+    if (!workspace || ws_bytes < w.plain) return fail(ctx, SD_ERR_WORKSPACE, "workspace too small");
     DeviceGuard dg(ctx->device);
     sd::SelectArgs a{};
     a.page_table = page_table;
@@ -542,7 +545,7 @@ sd_status sparse_decode_attend_noalloc(sd_ctx *ctx, const void *q, const void *k
       return fail(ctx, SD_ERR_INVALID_ARG, "q, k_cache and v_cache must be 16-byte aligned");
     if (ctx->sh.H_ret > 0 && (!sel_idx || !sel_count || sel_stride <= 0))
       return fail(ctx, SD_ERR_INVALID_ARG, "selection lists required for retrieval heads");
-    const size_t need = sd::attend_workspace_bytes(ctx->sh, ctx->tb, batch);
+    const size_t need = sd::attend_workspace_bytes(ctx->sh, ctx->tb, batch, false);
     if (need > sd::kNoAllocScratchBytes)
       return fail(ctx, SD_ERR_WORKSPACE,
                   "attend needs " + std::to_string(need) + " bytes of scratch for this batch; the built-in scratch holds " +

@@ -920,7 +920,8 @@ AttParams att_params(const Shape &sh, const Tables &tb, int batch) {
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct AttLayout {
-  size_t partials, plan_row, plan_mask, plan_cnt, tstart, counters, seg, total;
+  size_t partials, plan_row, plan_mask, plan_cnt, tstart, counters, plain;
+  size_t seg, total;                                                  // the CTAs' shares: behind what every call uses
   size_t logits, tile_row, tile_item, lse, total_mass;                // accumulated weights: behind the rest
 };
 
@@ -936,6 +937,7 @@ AttLayout att_layout(const Shape &sh, const Tables &tb, int batch, long long loc
   L.plan_cnt = o;  o = align256(o + (size_t)batch * tb.n_ret * p.ns * 4);
   L.tstart = o;    o = align256(o + (size_t)(p.ni + 1) * 8);
   L.counters = o;  o = align256(o + (size_t)p.ni * 2 * 4);           // item_rows, tickets
+  L.plain = o;
   L.seg = o;       o = align256(o + (size_t)std::max(kMaxSegments, p.ni + 1) * sizeof(Segment) + (size_t)(p.ni + 2) * 4);
   L.total = o;
   const size_t loc_tiles = (size_t)((std::min(sh.max_len, local_rows) + kTileRows - 1) / kTileRows);
@@ -1013,8 +1015,9 @@ cudaError_t dispatch_gr(const AttendArgs &a, const Shape &sh, const Tables &tb, 
 
 }  // namespace
 
-size_t attend_workspace_bytes(const Shape &sh, const Tables &tb, int batch) {
-  return att_layout(sh, tb, batch, 0).total;
+size_t attend_workspace_bytes(const Shape &sh, const Tables &tb, int batch, bool shares) {
+  const AttLayout L = att_layout(sh, tb, batch, 0);
+  return shares ? L.total : L.plain;
 }
 
 size_t attend_mass_workspace_bytes(const Shape &sh, const Tables &tb, int batch, long long local_rows) {

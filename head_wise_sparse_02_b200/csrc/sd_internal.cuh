@@ -360,7 +360,9 @@ cudaError_t launch_local_append(const uint16_t *k_new, const uint16_t *v_new, co
                                 const Shape &sh, const Tables &tb, int max_batch, int num_sinks, int window,
                                 unsigned *err, cudaStream_t st);
 
-size_t attend_workspace_bytes(const Shape &sh, const Tables &tb, int batch);
+// shares: with the CTAs' shares of the items, which only the calls on 4-bit records
+// and those that accumulate weights write
+size_t attend_workspace_bytes(const Shape &sh, const Tables &tb, int batch, bool shares);
 // with accumulated weights (AttendArgs::mass); local_rows = num_sinks + window
 size_t attend_mass_workspace_bytes(const Shape &sh, const Tables &tb, int batch, long long local_rows);
 // plan_only: null = plan every retrieval item; else the select's miss array

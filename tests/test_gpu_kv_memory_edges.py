@@ -12,7 +12,7 @@ import pytest
 import torch
 
 from tests.test_gpu_evict import Pool
-from tests.test_gpu_kv4 import Case
+from tests.test_gpu_kv4 import Case, _context, _gen, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -141,3 +141,38 @@ def test_results_do_not_depend_on_the_context_that_ran_first():
         return [line for line in r.stdout.splitlines() if line.startswith("bits")][0]
     assert bits(f"{1 << 21}") == bits(f"6000,{1 << 21}")
     assert bits("6000") == bits(f"{1 << 21},6000")
+
+
+# ------------------------------------------------------------------ workspaces of the plain calls
+
+def test_plain_calls_take_no_more_workspace_than_they_read():
+    """The shares of the calls that take one item per CTA come last: the plain bf16
+    calls do without them, in a caller's workspace and in the built-in scratch."""
+    from head_wise_sparse_02_b200 import sparse_decode as sd
+    B, d, maxp = 36000, 64, 16
+    ctx = _context([1], 1, d, 8, maxp, B, mode="top_k", top_k=4)
+    k, v, q = _randn((8, 1, 16, d), 1), _randn((8, 1, 16, d), 2), _randn((B, 1, d), 3)
+    table = torch.randint(0, 8, (B, maxp), generator=_gen(4), device="cuda", dtype=torch.int32)
+    lens = torch.randint(4, 17, (B,), generator=_gen(5), device="cuda", dtype=torch.int32)
+    sel = torch.tensor([0, 1, 2, 3], dtype=torch.int32, device="cuda").expand(B, 1, 4).contiguous()
+    cnt = torch.randint(0, 5, (B, 1), generator=_gen(6), device="cuda", dtype=torch.int32)
+    # partial results, union lists of one span, counts, first tiles and counters
+    a256 = lambda x: (x + 255) // 256 * 256
+    need = a256((4096 + B) * (d + 2) * 4) + a256(B * 256 * 4) + a256(B * 256 * 2) + a256(B * 4) + a256((B + 1) * 8) + a256(B * 8)
+    assert need < 64 << 20 < need + B * 36
+    ref, out = torch.full((B, 1, d), float("nan"), device="cuda"), torch.full((B, 1, d), float("nan"), device="cuda")
+    ws = ctx.alloc(B)[0]
+    ctx.attend(q, k, v, table, lens, sel, cnt, ref, ws)
+    sd.sparse_decode_attend_noalloc(ctx.handle, q, k, v, table, lens, sel, cnt, out)
+    torch.cuda.synchronize()
+    assert ctx.error_word() == 0 and torch.isfinite(ref).all() and torch.equal(out, ref)
+    out.fill_(float("nan"))
+    short = ws[:ws.numel() - B * 32].clone()
+    ctx.attend(q, k, v, table, lens, sel, cnt, out, short)
+    torch.cuda.synchronize()
+    assert ctx.error_word() == 0 and torch.equal(out, ref)
+    kv4 = ctx.kv4_cache()
+    with pytest.raises(sd.SparseDecodeError) as e:
+        ctx.attend_kv4(q, kv4, table, lens, sel, cnt, out, short)
+    assert e.value.status == sd.SD_ERR_WORKSPACE
+    ctx.close()
