@@ -409,6 +409,24 @@ def _check_batch(q, out, page_table, seq_lens) -> int:
     return B
 
 
+def _check_kv(k_cache, v_cache, d: int) -> None:
+    """Both caches are [num_pages, Hkv, page, d]."""
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[3] != d or v_cache.shape != shape:
+        raise ValueError(f"k_cache and v_cache must be [num_pages, Hkv, page, d = {d}], got {tuple(shape)} / "
+                         f"{tuple(v_cache.shape)}")
+
+
+def _check_index(q_pre, q, index_cache, cache) -> None:
+    """The selection's inputs (None without retrieval heads): q_pre lies like q, the
+    index like the cache's rows."""
+    if q_pre is not None and q_pre.shape != q.shape:
+        raise ValueError(f"q_pre must be like q {tuple(q.shape)}, got {tuple(q_pre.shape)}")
+    if index_cache is not None and index_cache.shape != cache.shape[:3] + (16,):
+        raise ValueError(f"index_cache must be [num_pages, Hkv, page, 16] like the cache {tuple(cache.shape[:3])}, got "
+                         f"{tuple(index_cache.shape)}")
+
+
 def _check_mass(mass, cache) -> None:
     """Accumulated weights lie like the caches' rows: [num_pages, Hkv, page]."""
     if mass is not None and mass.shape != cache.shape[:3]:
@@ -463,6 +481,7 @@ def sparse_decode_select_attend_kv4(ctx: int, q_pre, q, index_cache, kv4_cache, 
     _check_sets(ctx, sel_idx, sel_count, B)
     _check_kv4(kv4_cache, None, q.shape[2])
     _check_mass(mass, kv4_cache)
+    _check_index(q_pre, q, index_cache, kv4_cache)
     dev = q.get_device()
     _check(LIB.sparse_decode_select_attend_kv4(
         ctx, _fast(q_pre, torch.bfloat16, "q_pre", dev), _fast(q, torch.bfloat16, "q", dev),
@@ -479,6 +498,7 @@ def sparse_decode_attend_mass(ctx: int, q, k_cache, v_cache, page_table, seq_len
     """attend that adds every attention weight to mass [num_pages, Hkv, page]."""
     B = _check_batch(q, out, page_table, seq_lens)
     _check_sets(ctx, sel_idx, sel_count, B)
+    _check_kv(k_cache, v_cache, q.shape[2])
     _check_mass(mass, k_cache)
     dev = q.get_device()
     _check(LIB.sparse_decode_attend_mass(
@@ -495,7 +515,9 @@ def sparse_decode_select_attend_mass(ctx: int, q_pre, q, index_cache, k_cache, v
     """select followed by attend_mass on the same sets, in one call."""
     B = _check_batch(q, out, page_table, seq_lens)
     _check_sets(ctx, sel_idx, sel_count, B)
+    _check_kv(k_cache, v_cache, q.shape[2])
     _check_mass(mass, k_cache)
+    _check_index(q_pre, q, index_cache, k_cache)
     dev = q.get_device()
     _check(LIB.sparse_decode_select_attend_mass(
         ctx, _fast(q_pre, torch.bfloat16, "q_pre", dev), _fast(q, torch.bfloat16, "q", dev),
@@ -736,22 +758,20 @@ class SparseDecode:
                           workspace, mass=None, stream=None):
         self._step(q, page_table)
         self._own(kv4_cache.shape, self._records, "kv4_cache")
-        if index_cache is not None:                          # None without retrieval heads
-            self._own(index_cache.shape, self._index_rows, "index_cache")
         sparse_decode_select_attend_kv4(self.handle, q_pre, q, index_cache, kv4_cache, page_table, seq_lens, sel_idx,
                                         sel_count, out, workspace, mass, stream)
 
     def attend_mass(self, q, k_cache, v_cache, page_table, seq_lens, sel_idx, sel_count, out, mass, workspace,
                     stream=None):
         self._step(q, page_table)
-        self._own(mass.shape, self._rows, "mass")
+        self._own(k_cache.shape, self._kv_rows, "k_cache")
         sparse_decode_attend_mass(self.handle, q, k_cache, v_cache, page_table, seq_lens, sel_idx, sel_count, out,
                                   mass, workspace, stream)
 
     def select_attend_mass(self, q_pre, q, index_cache, k_cache, v_cache, page_table, seq_lens, sel_idx, sel_count,
                            out, mass, workspace, stream=None):
         self._step(q, page_table)
-        self._own(mass.shape, self._rows, "mass")
+        self._own(k_cache.shape, self._kv_rows, "k_cache")
         sparse_decode_select_attend_mass(self.handle, q_pre, q, index_cache, k_cache, v_cache, page_table, seq_lens,
                                          sel_idx, sel_count, out, mass, workspace, stream)
 
