@@ -709,7 +709,13 @@ class SparseDecode:
         if shape != want:
             raise ValueError(f"{name} must be {want}, got {tuple(shape)}")
 
+    def _here(self, t, name):
+        """The other tensors of a call are compared with this one's device."""
+        if t.get_device() != self._dev:
+            raise ValueError(f"{name} must be on the context's device cuda:{self._dev}, got {t.device}")
+
     def _step(self, q, page_table):
+        self._here(q, "q")
         self._own(q.shape[1:], self._heads, "q[1:]")
         self._own(page_table.shape[1:], self._maxp, "page_table[1:]")
 
@@ -776,11 +782,13 @@ class SparseDecode:
                                          sel_idx, sel_count, out, mass, workspace, stream)
 
     def mass_clear(self, mass, slots, stream=None):
+        self._here(mass, "mass")
         self._own(mass.shape, self._rows, "mass")
         sparse_decode_mass_clear(self.handle, mass, slots, stream)
 
     def evict(self, mass, page_table, seq_lens, new_page_table, budget, keep_first, keep_last, kept, new_lens,
               k_cache=None, v_cache=None, index_cache=None, kv4_cache=None, stream=None):
+        self._here(mass, "mass")
         self._own(mass.shape, self._rows, "mass")
         self._own(page_table.shape[1:], self._maxp, "page_table[1:]")
         for t, want, name in ((k_cache, self._kv_rows, "k_cache"), (v_cache, self._kv_rows, "v_cache"),

@@ -176,3 +176,29 @@ def test_plain_calls_take_no_more_workspace_than_they_read():
         ctx.attend_kv4(q, kv4, table, lens, sel, cnt, out, short)
     assert e.value.status == sd.SD_ERR_WORKSPACE
     ctx.close()
+
+
+# ------------------------------------------------------------------ devices
+
+def test_calls_refuse_tensors_of_another_device_than_the_context():
+    p = Pool([40], 16, 2, 64, "plain", seed=1)
+    c = Case([50], 2, 1, 64, [1, 0], 8, 1, seed=1)
+    slots = torch.zeros(1, dtype=torch.int32, device="cuda")
+    row, pre = torch.zeros((1, 1, 64), dtype=torch.bfloat16, device="cuda"), c.q.clone()
+    index = torch.zeros(c.kv4.shape[:3] + (16,), dtype=torch.bfloat16, device="cuda")
+    sets = (c.table, c.seq_lens, c.sel_idx, c.sel_count, c.out)
+    calls = [lambda: c.run("kv4", True), lambda: c.run("bf16", True),
+             lambda: c.sd.select_attend_kv4(pre, c.q, index, c.kv4, *sets, c.ws),
+             lambda: c.sd.select_attend_mass(pre, c.q, index, c.k_cache, c.v_cache, *sets, c.mass, c.ws),
+             lambda: c.sd.mass_clear(c.mass, slots), lambda: c.sd.kv4_append(row, row, slots, c.kv4),
+             lambda: c.sd.kv4_load(c.kv4, slots, row, row), lambda: p.run(2, 2)]
+    here = c.sd._dev
+    c.sd._dev = p.sd._dev = here + 1                                   # as if the contexts were on the next device
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError, match=f"cuda:{here + 1}, got"):
+            call()
+    c.sd._dev = p.sd._dev = here
+    c.run("kv4", True)
+    c.check("kv4", True)
+    c.sd.close()
+    p.sd.close()

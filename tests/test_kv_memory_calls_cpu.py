@@ -15,7 +15,9 @@ class Unreached:
     """Stands for the library: no call may get this far."""
 
     def __getattr__(self, name):
-        raise AssertionError(f"{name} was reached")
+        def call(*args):
+            raise AssertionError(f"{name} was reached")
+        return call
 
 
 @pytest.fixture
@@ -24,7 +26,7 @@ def ctx(monkeypatch):
     monkeypatch.setattr(sd, "sparse_decode_num_retrieval_heads", lambda ctx: HRET)
     monkeypatch.setattr(sd, "sparse_decode_destroy", lambda ctx: None)
     monkeypatch.setattr(sd, "LIB", Unreached())
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)      # the device number of the tensors here
     s = sd.SparseDecode(num_q_heads=HQ, num_kv_heads=HKV, head_dim=D, head_is_retrieval=[1, 1, 0, 0], num_pages=PAGES,
                         max_batch=B, max_pages_per_seq=MAXP, proj=torch.zeros((HKV, D, 16), dtype=torch.bfloat16))
     yield s
@@ -79,3 +81,19 @@ def test_every_shape_is_checked_by_the_call_of_the_library(ctx, call):
             t[name] = torch.zeros(shape, dtype=t[name].dtype)
             with pytest.raises(ValueError, match=r"must .*got"):
                 getattr(sd, "sparse_decode_" + call)(1, *(t[a] for a in CALLS[call]))
+
+
+@pytest.mark.parametrize("call", [*CALLS, "kv4_append", "kv4_load", "mass_clear", "evict"])
+def test_tensors_on_another_device_than_the_context(ctx, call):
+    """All on one device, but not the context's: its kernels would run on the wrong one."""
+    t = _tensors()
+    rows = [torch.zeros((2, HKV, D), dtype=torch.bfloat16) for _ in range(2)]
+    slots = torch.zeros(2, dtype=torch.int32)
+    args = {"kv4_append": (*rows, slots, t["kv4_cache"]), "kv4_load": (t["kv4_cache"], slots, *rows),
+            "mass_clear": (t["mass"], slots),
+            "evict": (t["mass"], t["page_table"], t["seq_lens"], t["page_table"].clone(), 8, 1, 1,
+                      torch.zeros((B, HKV, 8), dtype=torch.int32), torch.zeros(B, dtype=torch.int32))}
+    ctx._dev = 0
+    ctx_call = getattr(ctx, call)
+    with pytest.raises(ValueError, match="cuda:0, got|must be a CUDA tensor"):
+        ctx_call(*(args[call] if call in args else (t[a] for a in CALLS[call])))
