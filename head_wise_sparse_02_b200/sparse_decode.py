@@ -132,6 +132,13 @@ def _fast(t: Optional[torch.Tensor], dtype: torch.dtype, name: str, dev: int) ->
     return _ptr(t, dtype, name, dev)
 
 
+def _int32(x: int, name: str) -> int:
+    """A number that the library takes as an int: ctypes would drop the upper bits."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
 def _check_sets(ctx: int, sel_idx, sel_count, batch: int) -> None:
     """With retrieval heads, sel_idx must be [>= B, H_ret, stride] and sel_count
     [>= B, H_ret]: the library addresses row (b, i) at (b * H_ret + i) * stride
@@ -533,9 +540,10 @@ def sparse_decode_mass_clear(ctx: int, mass: torch.Tensor, slots: torch.Tensor, 
     """Zero the accumulated weights of the slots that new tokens take."""
     if mass.dim() != 3:
         raise ValueError(f"mass must be [num_pages, Hkv, page], got {tuple(mass.shape)}")
+    T = _int32(slots.numel(), "slots' length")
     dev = mass.get_device()
     _check(LIB.sparse_decode_mass_clear(ctx, _fast(mass, torch.float32, "mass", dev),
-                                        _fast(slots, torch.int32, "slots", dev), slots.numel(), _stream(stream, dev)), ctx)
+                                        _fast(slots, torch.int32, "slots", dev), T, _stream(stream, dev)), ctx)
 
 
 def sparse_decode_evict(ctx: int, mass, page_table, seq_lens, new_page_table, budget: int, keep_first: int,
@@ -545,6 +553,8 @@ def sparse_decode_evict(ctx: int, mass, page_table, seq_lens, new_page_table, bu
     weight, moving the kept rows of the given caches to the pages of
     new_page_table.  kept int32 [>= B, Hkv, budget], new_lens int32 [>= B]."""
     B, shape = seq_lens.numel(), mass.shape
+    for name, x in (("budget", budget), ("keep_first", keep_first), ("keep_last", keep_last)):
+        _int32(x, name)
     if len(shape) != 3:
         raise ValueError(f"mass must be [num_pages, Hkv, page], got {tuple(shape)}")
     if kept.dim() != 3 or kept.shape[0] < B or kept.shape[1] != shape[1] or kept.shape[2] != budget:

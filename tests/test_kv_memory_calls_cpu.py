@@ -98,3 +98,14 @@ def test_tensors_on_another_device_than_the_context(ctx, call):
     want = "must be a CUDA tensor" if call.startswith("kv4_") else "the context's device cuda:0, got cpu"
     with pytest.raises(ValueError, match=want):
         getattr(ctx, call)(*(args[call] if call in args else (t[a] for a in CALLS[call])))
+
+
+@pytest.mark.parametrize("kw", [dict(keep_first=2 ** 32), dict(keep_last=2 ** 32 + 1), dict(keep_last=-2 ** 32), dict(budget=2 ** 32 + 8)])
+def test_numbers_beyond_32_bits_are_refused(ctx, kw):
+    t = _tensors()
+    args = dict(budget=8, keep_first=1, keep_last=1) | kw
+    with pytest.raises(ValueError, match="must fit 32 bits"):
+        ctx.evict(t["mass"], t["page_table"], t["seq_lens"], t["page_table"].clone(), kept=torch.zeros((B, HKV, 8), dtype=torch.int32),
+                  new_lens=torch.zeros(B, dtype=torch.int32), **args)
+    with pytest.raises(ValueError, match="must fit 32 bits"):          # a length without memory behind it
+        ctx.mass_clear(t["mass"], torch.zeros(1, dtype=torch.int32).expand(2 ** 32))
