@@ -98,33 +98,35 @@ class DecodeStep:
     def make_split(self, stream=None):
         """Build the split layout from the full caches: k_ret / v_ret keep the
         retrieval KV groups, and local_append copies every sequence's sinks
-        and window (its local positions, in order) into compacted caches."""
-        retr = self.sd.cfg["head_is_retrieval"]
-        Hkv = self.k_cache.shape[1]
-        G = self.num_q_heads // Hkv
-        ret_g = [g for g in range(Hkv) if any(retr[g * G:(g + 1) * G])]
-        if ret_g == list(range(Hkv)):                                  # every group retrieves
-            self.k_ret, self.v_ret = self.k_cache, self.v_cache
-        else:
-            self.k_ret = self.k_cache[:, ret_g].contiguous()
-            self.v_ret = self.v_cache[:, ret_g].contiguous()
-        self.local_k, self.local_v = self.sd.local_cache()
-        window, sinks = self.sd.cfg.get("window", 0), self.sd.cfg.get("num_sinks", 0)
-        lens = self.seq_lens.tolist()
-        seq, pos = [], []
-        for b, n in enumerate(lens):
-            keep = sorted(set(range(min(sinks, n))) | set(range(max(0, n - window), n)))
-            seq += [b] * len(keep)
-            pos += keep
-        if pos:
-            dev = self.k_cache.device
-            seq_t = torch.tensor(seq, dtype=torch.int32, device=dev)
-            pos_t = torch.tensor(pos, dtype=torch.int32, device=dev)
-            page = self.page_table[seq_t.long(), (pos_t // 16).long()].long()
-            off = (pos_t % 16).long()
-            k_new = self.k_cache[page, :, off].contiguous()           # [T, Hkv, d]
-            v_new = self.v_cache[page, :, off].contiguous()
-            self.sd.local_append(k_new, v_new, seq_t, pos_t, self.local_k, self.local_v, stream)
+        and window (its local positions, in order) into compacted caches.  All
+        of it runs on `stream`."""
+        with _on(stream, self.k_cache.device):
+            retr = self.sd.cfg["head_is_retrieval"]
+            Hkv = self.k_cache.shape[1]
+            G = self.num_q_heads // Hkv
+            ret_g = [g for g in range(Hkv) if any(retr[g * G:(g + 1) * G])]
+            if ret_g == list(range(Hkv)):                                  # every group retrieves
+                self.k_ret, self.v_ret = self.k_cache, self.v_cache
+            else:
+                self.k_ret = self.k_cache[:, ret_g].contiguous()
+                self.v_ret = self.v_cache[:, ret_g].contiguous()
+            self.local_k, self.local_v = self.sd.local_cache()
+            window, sinks = self.sd.cfg.get("window", 0), self.sd.cfg.get("num_sinks", 0)
+            lens = self.seq_lens.tolist()
+            seq, pos = [], []
+            for b, n in enumerate(lens):
+                keep = sorted(set(range(min(sinks, n))) | set(range(max(0, n - window), n)))
+                seq += [b] * len(keep)
+                pos += keep
+            if pos:
+                dev = self.k_cache.device
+                seq_t = torch.tensor(seq, dtype=torch.int32, device=dev)
+                pos_t = torch.tensor(pos, dtype=torch.int32, device=dev)
+                page = self.page_table[seq_t.long(), (pos_t // 16).long()].long()
+                off = (pos_t % 16).long()
+                k_new = self.k_cache[page, :, off].contiguous()           # [T, Hkv, d]
+                v_new = self.v_cache[page, :, off].contiguous()
+                self.sd.local_append(k_new, v_new, seq_t, pos_t, self.local_k, self.local_v, stream)
 
     def attend_split(self, q: torch.Tensor, sel_idx=None, sel_count=None, stream=None):
         self.sd.attend_split(q, self.k_ret, self.v_ret, self.local_k, self.local_v, self.page_table,

@@ -188,3 +188,29 @@ def test_calls_that_do_not_accumulate_leave_the_weights():
 def _weights(st, b, g, n):
     pg = st.page_table[b].long().repeat_interleave(16)[:n]
     return st.mass[pg, g, torch.arange(n, device="cuda") % 16].double().cpu().numpy()
+
+
+def test_split_layout_made_on_a_side_stream_while_the_current_one_is_busy(monkeypatch):
+    """The rows that the append reads are gathered on its own stream: work queued on
+    the current one between the two (here after the positions) holds nothing up."""
+    from head_wise_sparse_02_b200 import decode
+    st, _ = _step(lens=(250, 131), window=40)
+    st.make_split()
+    torch.cuda.synchronize()
+    names = ("k_ret", "v_ret", "local_k", "local_v")
+    want = [getattr(st, n).clone() for n in names]
+    tensor = torch.tensor
+
+    def slow(*args, **kw):
+        t = tensor(*args, **kw)
+        torch.cuda._sleep(BUSY)
+        return t
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with monkeypatch.context() as m:
+        m.setattr(decode.torch, "tensor", slow)
+        st.make_split(side)
+    torch.cuda.synchronize()
+    assert st.error_word() == 0
+    assert all(torch.equal(getattr(st, n), w) for n, w in zip(names, want))
+    st.close()
