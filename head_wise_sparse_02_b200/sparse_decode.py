@@ -553,8 +553,9 @@ def sparse_decode_evict(ctx: int, mass, page_table, seq_lens, new_page_table, bu
     weight, moving the kept rows of the given caches to the pages of
     new_page_table.  kept int32 [>= B, Hkv, budget], new_lens int32 [>= B]."""
     B, shape = seq_lens.numel(), mass.shape
-    for name, x in (("budget", budget), ("keep_first", keep_first), ("keep_last", keep_last)):
-        _int32(x, name)
+    if (budget | keep_first | keep_last) >> 31:                # one beyond 32 bits, or negative (for the library)
+        for name, x in (("budget", budget), ("keep_first", keep_first), ("keep_last", keep_last)):
+            _int32(x, name)
     if len(shape) != 3:
         raise ValueError(f"mass must be [num_pages, Hkv, page], got {tuple(shape)}")
     if kept.dim() != 3 or kept.shape[0] < B or kept.shape[1] != shape[1] or kept.shape[2] != budget:
