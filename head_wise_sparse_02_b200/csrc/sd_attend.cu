@@ -28,7 +28,9 @@
 //   main  a persistent grid, one CTA per resident slot.  CTA c takes the
 //         equal share [W c / P, W (c + 1) / P) of all W tiles and walks the
 //         items it overlaps (usually one or two), so that its rings run
-//         without the start and drain of a grid of small CTAs.  Four warps
+//         without the start and drain of a grid of small CTAs.  (The form that
+//         keeps the weights, and the 4-bit kernel, take one share of one item
+//         per CTA instead, as the layout has written it.)  Four warps
 //         stream tiles through per-warp cp.async rings (whole rows per
 //         instruction, padded row pitch; each warp fetches its tiles' rows
 //         from the union lists itself, one tile ahead, so nothing stops the
@@ -123,8 +125,8 @@ __device__ void item_prefix(const AttendArgs &a, const Shape &sh, const Tables &
 // enough that all fit the grid.  `grid` CTAs are resident at once; many items take
 // several times that, so that an item of average size still has more than one CTA.
 // A CTA takes at least this many tiles before an item gets another: twice as many
-// of the 4-bit tiles, which are a third of the bytes (B 4, 32K: 28.4 us at 8, 26.0
-// at 16, 28.0 at 32; bf16 with weights, B 3, 2K: 23.8 at 8, 32.2 at 16).
+// of the 4-bit tiles, which are a third of the bytes (B 4, 32K: 27.2 us at 8, 25.5
+// at 16, 28.5 at 32; bf16 with weights, B 3, 2K: 23.8 at 8, 32.2 at 16).
 constexpr int kMinSegTiles = 8, kMinSegTiles4 = 16;
 
 template <typename T>

@@ -47,7 +47,7 @@ namespace {
 
 constexpr int kWarps4 = 4;
 constexpr int kThreads4 = kWarps4 * 32;
-constexpr int kRing4 = 2;               // tiles in flight per warp (B 16, 128K, 2%: 70.8 us; 3: 73.5, 4: 74.1)
+constexpr int kRing4 = 2;               // tiles in flight per warp (B 16, 128K, 2%: 69.8 us; 3: 70.7, 4: 73.2)
 constexpr float kLazy = 4.0f;           // a head's reference may lag its maximum by this (log2)
 constexpr int kScaleTop = 10;           // exponent of the largest p s at p = 1
 // the nibbles at bits 0-3 (low) and 4-7 (high) of both halves of w, as f16: code - 8
@@ -140,9 +140,10 @@ __device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_ui
 //                        [span prefix of the item: ns + 1 ints, rounded up to 16 bytes]
 //                        [query fragments: d / 32 x 2 x 32 lanes x 16 bytes]
 // at the end the ring holds the warps' (m, l, acc) for the CTA merge.
-// CTAs per SM: 3 of up to four heads (4, with fewer registers: 78 us instead of
-// 71 at B 16, 128K), 4 of up to eight (3: 72.4 instead of 70.7 us on a ragged batch
-// of 33), 2 of sixteen.
+// CTAs per SM: 3 of up to four heads (4, with fewer registers: 26.5 us instead of
+// 25.5 at B 4, 32K, 70.2 instead of 69.8 at B 16, 128K), 4 of up to eight (3: 71.5
+// instead of 67.4 us on a ragged batch of 33, although d = 128 spills 24 to 28 bytes
+// of stores at four), 2 of sixteen.
 template <int D, int GR, bool MASS>
 __global__ void __launch_bounds__(kThreads4, GR > 8 ? 2 : GR > 4 ? 4 : 3)
 attend_kv4_kernel(const AttendArgs a, const Shape sh, const Tables tb, const AttParams ap, const AttWs ws, int gr) {

@@ -27,6 +27,12 @@ class DecodeStep:
 
     k_cache / v_cache: bf16 [num_pages, Hkv, 16, d]; page_table int32 [B, MAXP];
     seq_lens int32 [B]; proj bf16 [Hkv, d, 16].
+
+    The bf16 caches are the caller's, who writes every new token's rows there
+    before a call that reads them (step, attend, select_exact, make_kv4, ...);
+    no method does.  step_kv4 appends to the 4-bit cache and reads that alone:
+    tokens stepped with it are in the bf16 caches only if the caller wrote them
+    there too, and tokens stepped with `step` are not in the 4-bit cache.
     """
 
     def __init__(self, *, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,

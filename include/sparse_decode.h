@@ -191,8 +191,9 @@ SD_API sd_status sparse_decode_init(const sd_config *cfg, const void *proj, sd_c
 
 /*
  * sparse_decode_workspace_size -- bytes of device workspace that select and
- * attend need for a batch of `batch` sequences (batch <= max_batch).  The
- * same workspace serves both calls.  `bytes` receives the size.
+ * attend, on bf16 or 4-bit caches, need for a batch of `batch` sequences
+ * (batch <= max_batch).  The same workspace serves all of them.  `bytes`
+ * receives the size.
  */
 SD_API sd_status sparse_decode_workspace_size(const sd_ctx *ctx, int batch, size_t *bytes);
 
@@ -280,7 +281,8 @@ SD_API sd_status sparse_decode_select_exact(sd_ctx *ctx, const void *q, const vo
  * written by sparse_decode_select or by the caller) and the sinks + window of a
  * local head.  One softmax over the whole set; fp32 accumulation; an empty
  * set gives zeros.  Each KV row of a GQA group is read once per call even
- * when several heads of the group selected it.
+ * when several heads of the group selected it.  The rows of every set hold
+ * finite keys and values.
  *
  *   q          device bf16 [B, Hq, d], post-RoPE queries.
  *   k_cache, v_cache, page_table, seq_lens   as described above.
@@ -509,8 +511,8 @@ SD_API sd_status sparse_decode_kv4_append(sd_ctx *ctx, const void *k_new, const 
  *
  *   k_out[t, g, :] = bf16_rne( lo + s * code )  of slot slots[t]
  *
- * (and likewise v), for the calls that take bf16 caches (prefill of a later
- * chunk, exact-score selection).
+ * (and likewise v): rows in the order of the slots, for the caller to use or to
+ * store where it wants them (the calls that take bf16 caches read whole caches).
  *
  *   k_out, v_out  device bf16 [num_tokens, Hkv, d], 16-byte aligned.
  *
@@ -530,8 +532,12 @@ SD_API sd_status sparse_decode_kv4_load(sd_ctx *ctx, const void *kv4_cache, cons
  *
  * Records that no append has written may hold NaN scales; they must not be
  * inside any head's set.
- * Queries, keys and values are below 2^100 in magnitude
- * (beyond, the kernel's powers of two overflow).
+ * Ranges: queries, keys and values are below 2^100 in magnitude (beyond, the
+ * kernel's powers of two overflow), and so that logits stay finite in float32,
+ * attn_scale * log2(e) * |q| |k| is below 2^126.  A query's elements are held to
+ * 2^-40 of its largest and to 2^-114, a weight times a value's scale to 2^-22 of
+ * itself and to 2^-34 of the largest scale that the head's own set has in the
+ * same 32 channels; rows that a head leaves out do not count for it.
  */
 SD_API sd_status sparse_decode_attend_kv4(sd_ctx *ctx, const void *q, const void *kv4_cache,
                                    const int32_t *page_table, const int32_t *seq_lens, int batch,
@@ -558,7 +564,9 @@ SD_API sd_status sparse_decode_select_attend_kv4(sd_ctx *ctx, const void *q_pre,
  *
  * Rows outside every set keep their value.  The sums are float32 and the same
  * in every run, unless sequences of the batch share pages: their weights then
- * all count, added in no fixed order.
+ * all count, added in no fixed order.  As for sparse_decode_attend, the rows of
+ * every set hold finite numbers: a NaN or an infinity in a value also reaches the
+ * heads of the KV group that leave the row out.
  *
  *   mass       device float32 [num_pages, Hkv, P], 16-byte aligned, updated in place.
  *   workspace  at least sparse_decode_mass_workspace_size bytes.

@@ -98,6 +98,19 @@ def test_values_a_head_leaves_out_do_not_cost_it_precision(d, G, power):
     c.sd.close()
 
 
+@pytest.mark.parametrize("kscale,qscale,vscale", [(2.0 ** 60, 2.0 ** 58, 1.0), (2.0 ** 95, 2.0 ** -95, 2.0 ** 95),
+                                                  (2.0 ** -95, 2.0 ** 95, 2.0 ** -95), (2.0 ** 95, 2.0 ** 20, 2.0 ** 95)])
+@pytest.mark.parametrize("d,G", [(128, 4), (64, 8), (128, 16)])
+def test_ends_of_the_documented_ranges(d, G, kscale, qscale, vscale):
+    """Logits up to 2^125 and operands up to 2^98 give finite outputs within the
+    tolerances (which say nothing of the weights once logits are that large)."""
+    c = Case([300, 40], G, 1, d, [1] * (G - 1) + [0], 100, 2, seed=d + G, kscale=kscale, qscale=qscale, vscale=vscale)
+    c.run("kv4", True)
+    c.check("kv4", True)
+    assert torch.isfinite(c.out).all() and torch.isfinite(c.mass).all()
+    c.sd.close()
+
+
 # ------------------------------------------------------------------ the same bits whatever ran before
 
 ORDER = """
