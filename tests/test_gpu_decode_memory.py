@@ -74,7 +74,7 @@ def test_memory_replaced_under_a_running_stream_is_not_handed_out():
     torch.cuda.synchronize()
     old = [(t.data_ptr(), t.numel() * t.element_size()) for t in (st.workspace, st.mass)]
     with torch.cuda.stream(side):
-        torch.cuda._sleep(BUSY)
+        torch.cuda._sleep(5 * BUSY)
     st.keep_mass(side)
     taken = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in old for _ in range(3)]
     assert not side.query()                                            # else the test would show nothing
